@@ -361,6 +361,137 @@ kvc_status kvc_step_scores(const kvc_cache *cache, const float *scores, const in
                        "kvc_step_scores launch");
 }
 
+size_t kvc_reserve_workspace_bytes(int32_t rows) { return rows < 0 ? 0 : ((size_t)rows + 1) * sizeof(int64_t); }
+
+kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, const int32_t *next_pos, uint8_t label,
+                             float *crf, const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
+                             int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                             int64_t *slot_map, void *workspace, size_t workspace_bytes, int32_t *d_status,
+                             kvc_stream_t stream) {
+    g_err[0] = 0;
+    kvc::CacheView c;
+    kvc_status s = view_cache(cache, c, true);
+    if (s != KVC_OK) return s;
+    if (!new_count || !next_pos || !free_pages || !free_count)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "new_count, next_pos, free_pages and free_count are required");
+    if (max_tokens < 0) return fail(KVC_ERR_INVALID_ARGUMENT, "max_tokens must be >= 0");
+    if (!row_len_out || !free_count_out || !token_start || (max_tokens > 0 && (!token_pos || !slot_map)))
+        return fail(KVC_ERR_INVALID_ARGUMENT,
+                    "row_len_out, free_count_out, token_start, token_pos and slot_map are required");
+    if (!workspace || workspace_bytes < kvc_reserve_workspace_bytes(c.rows) || ((uintptr_t)workspace & 7))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "workspace must be 8-byte aligned and at least %zu bytes",
+                    kvc_reserve_workspace_bytes(c.rows));
+    return cuda_status(kvc::launch_reserve(c, new_count, next_pos, label, crf, free_pages, free_count, max_tokens,
+                                           row_len_out, free_count_out, token_start, token_pos, slot_map,
+                                           static_cast<int64_t *>(workspace), d_status, (cudaStream_t)stream),
+                       "kvc_reserve_slots launch");
+}
+
+kvc_status kvc_norm_rope_write(const kvc_cache *cache, const void *qkv, int64_t token_stride, int32_t num_tokens,
+                               const int32_t *token_count, int32_t num_q_heads, const void *q_weight,
+                               const void *k_weight, float eps, const float *inv_freq, int32_t rope_dim, uint32_t flags,
+                               const int32_t *token_pos, const int64_t *slot_map, void *q_out, int32_t *d_status,
+                               kvc_stream_t stream) {
+    g_err[0] = 0;
+    kvc::CacheView c;
+    kvc_status s = view_cache(cache, c, true);
+    if (s != KVC_OK) return s;
+    if (num_tokens < 0) return fail(KVC_ERR_INVALID_ARGUMENT, "num_tokens must be >= 0");
+    if (num_q_heads <= 0 || num_q_heads % c.num_kv_heads != 0)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "num_q_heads must be a positive multiple of num_kv_heads");
+    if (num_q_heads / c.num_kv_heads > 128) return fail(KVC_ERR_UNSUPPORTED, "at most 128 query heads per KV head");
+    if (flags & ~KVC_ROPE_INTERLEAVED) return fail(KVC_ERR_INVALID_ARGUMENT, "unknown flags");
+    if (rope_dim < 0 || rope_dim > c.head_dim) return fail(KVC_ERR_INVALID_ARGUMENT, "rope_dim must be in [0, head_dim]");
+    if (rope_dim % 16) return fail(KVC_ERR_UNSUPPORTED, "rope_dim must be a multiple of 16");
+    if (rope_dim > 0 && !inv_freq) return fail(KVC_ERR_INVALID_ARGUMENT, "inv_freq is NULL");
+    if ((q_weight || k_weight) && (!(eps >= 0.f) || !std::isfinite(eps)))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+    if (num_tokens == 0) return KVC_OK;
+    if (!qkv || !token_pos || !slot_map || !q_out)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "qkv, token_pos, slot_map and q_out are required");
+    const int esize = c.dtype == KVC_BF16 ? 2 : 4;
+    const int64_t vec = (int64_t)c.num_layers * (num_q_heads + 2 * c.num_kv_heads) * c.head_dim;
+    if (vec > INT32_MAX) return fail(KVC_ERR_UNSUPPORTED, "more than 2^31 - 1 elements per token");
+    if (token_stride < vec || (token_stride * esize) % 16)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "token_stride must be at least %lld elements and a multiple of 16 bytes",
+                    (long long)vec);
+    if (((uintptr_t)qkv | (uintptr_t)q_out | (uintptr_t)q_weight | (uintptr_t)k_weight) & 15)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "qkv, q_out and the weights must be 16-byte aligned");
+    return cuda_status(kvc::launch_norm_rope(c, qkv, token_stride, num_tokens, token_count, num_q_heads, q_weight,
+                                             k_weight, eps, inv_freq, rope_dim, (flags & KVC_ROPE_INTERLEAVED) != 0,
+                                             token_pos, slot_map, q_out, d_status, (cudaStream_t)stream),
+                       "kvc_norm_rope_write launch");
+}
+
+kvc_status kvc_block_bounds(const kvc_cache *cache, const int32_t *from_len, void *bounds, int32_t *block_pos,
+                            int32_t *d_status, kvc_stream_t stream) {
+    g_err[0] = 0;
+    kvc::CacheView c;
+    kvc_status s = view_cache(cache, c, true);
+    if (s != KVC_OK) return s;
+    if (!bounds || !block_pos) return fail(KVC_ERR_INVALID_ARGUMENT, "bounds and block_pos are required");
+    if ((uintptr_t)bounds & 15) return fail(KVC_ERR_INVALID_ARGUMENT, "bounds must be 16-byte aligned");
+    return cuda_status(kvc::launch_block_bounds(c, from_len, bounds, block_pos, d_status, (cudaStream_t)stream),
+                       "kvc_block_bounds launch");
+}
+
+size_t kvc_select_blocks_workspace_bytes(int32_t rows, int32_t max_pages_per_row) {
+    return rows < 0 || max_pages_per_row < 0 ? 0 : (size_t)rows * (size_t)max_pages_per_row * sizeof(uint64_t);
+}
+
+kvc_status kvc_select_blocks(const kvc_cache *cache, const void *bounds, const int32_t *block_pos, const void *q,
+                             const int32_t *q_pos, int32_t num_q_heads, int32_t top_k, int32_t sink_blocks,
+                             int32_t recent_blocks, int32_t *block_list, int32_t *block_count, void *workspace,
+                             size_t workspace_bytes, int32_t *d_status, kvc_stream_t stream) {
+    g_err[0] = 0;
+    kvc::CacheView c;
+    kvc_status s = view_cache(cache, c, false);
+    if (s != KVC_OK) return s;
+    if (!bounds || !block_pos || !q || !q_pos || !block_list || !block_count)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "bounds, block_pos, q, q_pos, block_list and block_count are required");
+    if ((uintptr_t)bounds & 15) return fail(KVC_ERR_INVALID_ARGUMENT, "bounds must be 16-byte aligned");
+    if (num_q_heads <= 0 || num_q_heads % c.num_kv_heads != 0)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "num_q_heads must be a positive multiple of num_kv_heads");
+    if (num_q_heads / c.num_kv_heads > 128) return fail(KVC_ERR_UNSUPPORTED, "at most 128 query heads per KV head");
+    if (top_k <= 0 || top_k > (1 << 24)) return fail(KVC_ERR_INVALID_ARGUMENT, "top_k must be in [1, 2^24]");
+    if (sink_blocks < 0 || recent_blocks < 0 || (int64_t)sink_blocks + recent_blocks > top_k)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "sink_blocks and recent_blocks must be >= 0 and fit into top_k");
+    const size_t need = kvc_select_blocks_workspace_bytes(c.rows, c.max_pages_per_row);
+    if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 7))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "workspace must be 8-byte aligned and at least %zu bytes", need);
+    return cuda_status(kvc::launch_select_blocks(c, bounds, block_pos, q, q_pos, num_q_heads, top_k, sink_blocks,
+                                                 recent_blocks, block_list, block_count, workspace, d_status,
+                                                 (cudaStream_t)stream),
+                       "kvc_select_blocks launch");
+}
+
+size_t kvc_block_attention_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim) {
+    return rows < 0 || group <= 0 || head_dim <= 0 ? 0 : kvc::block_attention_workspace(rows, group, head_dim);
+}
+
+kvc_status kvc_block_attention(const kvc_cache *cache, const void *q, const int32_t *q_pos, int32_t num_q_heads,
+                               const int32_t *block_list, int32_t list_stride, const int32_t *block_count, float *out,
+                               float *lse, void *workspace, size_t workspace_bytes, int32_t *d_status,
+                               kvc_stream_t stream) {
+    g_err[0] = 0;
+    kvc::CacheView c;
+    kvc_status s = view_cache(cache, c, true);
+    if (s != KVC_OK) return s;
+    if (!q || !q_pos || !out || !lse) return fail(KVC_ERR_INVALID_ARGUMENT, "q, q_pos, out and lse are required");
+    if (num_q_heads <= 0 || num_q_heads % c.num_kv_heads != 0)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "num_q_heads must be a positive multiple of num_kv_heads");
+    const int group = num_q_heads / c.num_kv_heads;
+    if (group > 8) return fail(KVC_ERR_UNSUPPORTED, "at most 8 query heads per KV head");
+    if (block_list && (!block_count || list_stride <= 0))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "a block list needs block_count and a positive list_stride");
+    const size_t need = kvc::block_attention_workspace(c.rows, group, c.head_dim);
+    if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 7))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "workspace must be 8-byte aligned and at least %zu bytes", need);
+    return cuda_status(kvc::launch_block_attention(c, q, q_pos, num_q_heads, block_list, list_stride, block_count, out,
+                                                   lse, workspace, d_status, (cudaStream_t)stream),
+                       "kvc_block_attention launch");
+}
+
 kvc_status kvc_ratchet_init(void *state, int32_t *budget, int32_t num_seqs, const kvc_ratchet_params *params,
                             kvc_stream_t stream) {
     g_err[0] = 0;

@@ -103,6 +103,25 @@ cudaError_t launch_decode(const CacheView &c, const void *q, const int32_t *q_po
 cudaError_t launch_step_scores(const CacheView &c, const float *scores, const int32_t *step_start,
                                const int32_t *num_steps, int32_t max_steps, float beta, float *out, int32_t *status,
                                cudaStream_t stream);
+cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const int32_t *next_pos, uint8_t label, float *crf,
+                           const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
+                           int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                           int64_t *slot_map, int64_t *ws, int32_t *status, cudaStream_t stream);
+cudaError_t launch_norm_rope(const CacheView &c, const void *qkv, int64_t token_stride, int32_t num_tokens,
+                             const int32_t *token_count, int32_t num_q_heads, const void *q_weight, const void *k_weight,
+                             float eps, const float *inv_freq, int32_t rope_dim, bool interleaved,
+                             const int32_t *token_pos, const int64_t *slot_map, void *q_out, int32_t *status,
+                             cudaStream_t stream);
+cudaError_t launch_block_bounds(const CacheView &c, const int32_t *from_len, void *bounds, int32_t *block_pos,
+                                int32_t *status, cudaStream_t stream);
+cudaError_t launch_select_blocks(const CacheView &c, const void *bounds, const int32_t *block_pos, const void *q,
+                                 const int32_t *q_pos, int32_t num_q_heads, int32_t top_k, int32_t sink, int32_t recent,
+                                 int32_t *block_list, int32_t *block_count, void *ws, int32_t *status,
+                                 cudaStream_t stream);
+size_t block_attention_workspace(int64_t rows, int32_t group, int32_t head_dim);
+cudaError_t launch_block_attention(const CacheView &c, const void *q, const int32_t *q_pos, int32_t num_q_heads,
+                                   const int32_t *list, int32_t list_stride, const int32_t *list_len, float *out,
+                                   float *lse, void *ws, int32_t *status, cudaStream_t stream);
 cudaError_t launch_ratchet_init(void *state, int32_t *budget, int32_t num_seqs, const kvc_ratchet_params &p,
                                 cudaStream_t stream);
 cudaError_t launch_ratchet(const float *logits, int32_t num_seqs, int32_t steps, int32_t vocab, void *state,

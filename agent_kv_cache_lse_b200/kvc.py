@@ -22,14 +22,18 @@ KVC_OK, KVC_ERR_INVALID_ARGUMENT, KVC_ERR_UNSUPPORTED, KVC_ERR_CUDA, KVC_ERR_DEV
 KVC_F32, KVC_BF16 = 0, 1
 KVC_SCORE_ACCUMULATE, KVC_SCORE_COMPUTE_LSE, KVC_SCORE_SIMT = 1, 2, 4
 KVC_HIT_BINARY = 1
+KVC_ROPE_INTERLEAVED = 1
 DEV_CODES = {0: "ok", 1: "bad page", 2: "bad length", 3: "non-finite value", 4: "kept mismatch",
-             5: "freed list overflow", 6: "bad move", 7: "timeout", 8: "bad step table"}
+             5: "freed list overflow", 6: "bad move", 7: "timeout", 8: "bad step table", 9: "bad block list"}
 
 EXPORTS = ["kvc_status_string", "kvc_last_error", "kvc_version", "kvc_query_lse", "kvc_score_from_lse",
            "kvc_lrfu_update", "kvc_select_budget", "kvc_plan_slots", "kvc_compact_workspace_bytes",
            "kvc_compact_pages", "kvc_compact_pages_noalloc", "kvc_ratchet_state_bytes", "kvc_ratchet_init",
            "kvc_confidence_ratchet", "kvc_beacon_update", "kvc_lrfu_select", "kvc_decode_attention",
-           "kvc_step_scores", "kvc_append_workspace_bytes", "kvc_append_tokens", "kvc_select_plan"]
+           "kvc_step_scores", "kvc_append_workspace_bytes", "kvc_append_tokens", "kvc_select_plan",
+           "kvc_reserve_workspace_bytes", "kvc_reserve_slots", "kvc_norm_rope_write", "kvc_block_bounds",
+           "kvc_select_blocks_workspace_bytes", "kvc_select_blocks", "kvc_block_attention_workspace_bytes",
+           "kvc_block_attention"]
 
 
 class KvcCache(ctypes.Structure):
@@ -106,6 +110,17 @@ def lib() -> ctypes.CDLL:
             "kvc_append_workspace_bytes": (ctypes.c_size_t, [i32]),
             "kvc_append_tokens": (ctypes.c_int, [pc, vp, vp, vp, i32, ctypes.c_uint8, vp, vp, vp, vp, ctypes.c_size_t,
                                                  vp, vp]),
+            "kvc_reserve_workspace_bytes": (ctypes.c_size_t, [i32]),
+            "kvc_reserve_slots": (ctypes.c_int, [pc, vp, vp, ctypes.c_uint8, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+                                                 ctypes.c_size_t, vp, vp]),
+            "kvc_norm_rope_write": (ctypes.c_int, [pc, vp, i64, i32, vp, i32, vp, vp, f32, vp, i32, u32, vp, vp, vp, vp,
+                                                   vp]),
+            "kvc_block_bounds": (ctypes.c_int, [pc, vp, vp, vp, vp, vp]),
+            "kvc_select_blocks_workspace_bytes": (ctypes.c_size_t, [i32, i32]),
+            "kvc_select_blocks": (ctypes.c_int, [pc, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp,
+                                                 vp]),
+            "kvc_block_attention_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+            "kvc_block_attention": (ctypes.c_int, [pc, vp, vp, i32, vp, i32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -355,6 +370,172 @@ def kvc_step_scores(cache: Cache, scores: torch.Tensor, step_start: torch.Tensor
     _check(lib().kvc_step_scores(ctypes.byref(cs), _ptr(scores), _ptr(step_start), _ptr(num_steps),
                                  step_start.shape[1], beta, _ptr(out), _ptr(d_status), _stream(stream)),
            "kvc_step_scores")
+
+
+def _call(name: str, cache: Cache, args, tensors, stream):
+    """Call entry point `name` on the cache's device: `tensors` (name, tensor or None) must live there, and the call
+    goes to `stream` or that device's current stream."""
+    dev = cache.k_pool.device
+    for what, t in tensors:
+        if t is not None and t.device != dev:
+            raise KvcError(f"{what}: on {t.device}, the cache is on {dev}")
+    if dev.type != "cuda":
+        raise KvcError(f"{name}: the cache is on {dev}, expected a CUDA device")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, cache, args, (), stream)
+    st = torch.cuda.current_stream(dev) if stream is None else stream
+    st = st.cuda_stream if hasattr(st, "cuda_stream") else int(st)
+    cs = cache.struct()
+    _check(getattr(lib(), name)(ctypes.byref(cs), *args, st), name)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
+def kvc_reserve_workspace_bytes(rows: int) -> int:
+    return int(lib().kvc_reserve_workspace_bytes(rows))
+
+
+def kvc_reserve_slots(cache: Cache, new_count: torch.Tensor, next_pos: torch.Tensor, label: int,
+                      crf: Optional[torch.Tensor], free_pages: torch.Tensor, free_count: torch.Tensor,
+                      row_len_out: torch.Tensor, free_count_out: torch.Tensor, token_start: torch.Tensor,
+                      token_pos: torch.Tensor, slot_map: torch.Tensor, workspace: torch.Tensor, d_status=None,
+                      stream=None):
+    """Slots for new_count[s] new tokens of each sequence.  token_start: [S + 1] int32; token_pos: [max_tokens] int32;
+    slot_map: [max_tokens][L][Hkv] int64; row_len_out and free_count_out may be cache.row_len and free_count."""
+    S, T, i32 = cache.num_seqs, token_pos.numel(), torch.int32
+    _expect(new_count, "new_count", (S,), i32)
+    _expect(next_pos, "next_pos", (S,), i32)
+    if crf is not None:
+        _expect(crf, "crf", (cache.rows, cache.max_slots), torch.float32)
+    _expect(free_pages, "free_pages", (None,), i32)
+    _expect(free_count, "free_count", (1,), torch.int64)
+    _expect(row_len_out, "row_len_out", (cache.rows,), i32)
+    _expect(free_count_out, "free_count_out", (1,), torch.int64)
+    _expect(token_start, "token_start", (S + 1,), i32)
+    _expect(token_pos, "token_pos", (T,), i32)
+    _expect(slot_map, "slot_map", (T, cache.num_layers, cache.num_kv_heads), torch.int64)
+    if not 0 <= label <= 255:
+        raise KvcError(f"label: {label}, expected 0 to 255")
+    _call("kvc_reserve_slots", cache,
+          (_addr(new_count), _addr(next_pos), label, _addr(crf), _addr(free_pages), _addr(free_count), T,
+           _addr(row_len_out), _addr(free_count_out), _addr(token_start), _addr(token_pos), _addr(slot_map),
+           _addr(workspace), _nbytes(workspace), _addr(d_status)),
+          (("new_count", new_count), ("next_pos", next_pos), ("crf", crf), ("free_pages", free_pages),
+           ("free_count", free_count), ("row_len_out", row_len_out), ("free_count_out", free_count_out),
+           ("token_start", token_start), ("token_pos", token_pos), ("slot_map", slot_map), ("workspace", workspace),
+           ("d_status", d_status)), stream)
+
+
+def kvc_norm_rope_write(cache: Cache, qkv: torch.Tensor, token_pos: torch.Tensor, slot_map: torch.Tensor,
+                        q_out: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                        token_count: Optional[torch.Tensor] = None, d_status=None, stream=None):
+    """Norm and rotate the query and key heads of qkv [T][L][Hq + 2 Hkv][D] (tokens may be further apart than their
+    size: a slice of a wider array), queries to q_out [T][L][Hq][D], keys and values to the cache slots of slot_map
+    [T][L][Hkv].  inv_freq: [rope_dim / 2] fp32 or None for no rotation; token_count: one int32, the tokens present."""
+    L, Hkv, D, dt = cache.num_layers, cache.num_kv_heads, cache.k_pool.shape[2], cache.k_pool.dtype
+    if qkv.dim() != 4 or qkv.shape[1] != L or qkv.shape[3] != D or qkv.shape[2] <= 2 * Hkv:
+        raise KvcError(f"qkv: shape {tuple(qkv.shape)}, expected (*, {L}, Hq + {2 * Hkv}, {D})")
+    T, Hq = qkv.shape[0], qkv.shape[2] - 2 * Hkv
+    if qkv.dtype != dt:
+        raise KvcError(f"qkv: dtype {qkv.dtype}, expected {dt}")
+    stride = L * (Hq + 2 * Hkv) * D
+    if T > 1:
+        stride = max(stride, qkv.stride(0)) if qkv[0].is_contiguous() else -1
+        if stride != qkv.stride(0):
+            raise KvcError("qkv must be contiguous within a token, and tokens may not overlap")
+    elif not qkv.is_contiguous():
+        raise KvcError("qkv must be contiguous within a token")
+    _expect(q_out, "q_out", (T, L, Hq, D), dt)
+    _expect(token_pos, "token_pos", (T,), torch.int32)
+    _expect(slot_map, "slot_map", (T, L, Hkv), torch.int64)
+    for what, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _expect(w, what, (L, D), dt)
+    if inv_freq is not None:
+        _expect(inv_freq, "inv_freq", (None,), torch.float32)
+    if token_count is not None:
+        _expect(token_count, "token_count", (1,), torch.int32)
+    _call("kvc_norm_rope_write", cache,
+          (_addr(qkv), stride, T, _addr(token_count), Hq, _addr(q_weight), _addr(k_weight), eps, _addr(inv_freq),
+           0 if inv_freq is None else 2 * inv_freq.numel(), KVC_ROPE_INTERLEAVED if interleaved else 0,
+           _addr(token_pos), _addr(slot_map), _addr(q_out), _addr(d_status)),
+          (("qkv", qkv), ("token_pos", token_pos), ("slot_map", slot_map), ("q_out", q_out), ("q_weight", q_weight),
+           ("k_weight", k_weight), ("inv_freq", inv_freq), ("token_count", token_count), ("d_status", d_status)), stream)
+
+
+def kvc_block_bounds(cache: Cache, bounds: torch.Tensor, block_pos: torch.Tensor,
+                     from_len: Optional[torch.Tensor] = None, d_status=None, stream=None):
+    """Minimum and maximum of every page's keys: bounds [rows][max_pages][2][D] in the cache dtype, block_pos
+    [rows][max_pages] int32 (lowest position); from_len [rows] int32: only the pages from that slot on."""
+    rows, mp = cache.block_table.shape
+    _expect(bounds, "bounds", (rows, mp, 2, cache.k_pool.shape[2]), cache.k_pool.dtype)
+    _expect(block_pos, "block_pos", (rows, mp), torch.int32)
+    if from_len is not None:
+        _expect(from_len, "from_len", (rows,), torch.int32)
+    _call("kvc_block_bounds", cache, (_addr(from_len), _addr(bounds), _addr(block_pos), _addr(d_status)),
+          (("bounds", bounds), ("block_pos", block_pos), ("from_len", from_len), ("d_status", d_status)), stream)
+
+
+def kvc_select_blocks_workspace_bytes(rows: int, max_pages_per_row: int) -> int:
+    return int(lib().kvc_select_blocks_workspace_bytes(rows, max_pages_per_row))
+
+
+def kvc_select_blocks(cache: Cache, bounds: torch.Tensor, block_pos: torch.Tensor, q: torch.Tensor, q_pos: torch.Tensor,
+                      block_list: torch.Tensor, block_count: torch.Tensor, workspace: torch.Tensor,
+                      sink_blocks: int = 0, recent_blocks: int = 0, d_status=None, stream=None):
+    """The top_k = block_list.shape[1] pages of each row with the highest bound on the group's logits, the first
+    sink_blocks and last recent_blocks always among them: block_list [rows][top_k] int32 ascending, then -1;
+    block_count [rows] int32."""
+    rows, mp = cache.block_table.shape
+    D, dt = cache.k_pool.shape[2], cache.k_pool.dtype
+    _expect(bounds, "bounds", (rows, mp, 2, D), dt)
+    _expect(block_pos, "block_pos", (rows, mp), torch.int32)
+    _expect(q, "q", (cache.num_seqs, cache.num_layers, None, D), dt)
+    _expect(q_pos, "q_pos", (cache.num_seqs,), torch.int32)
+    _expect(block_list, "block_list", (rows, None), torch.int32)
+    _expect(block_count, "block_count", (rows,), torch.int32)
+    _call("kvc_select_blocks", cache,
+          (_addr(bounds), _addr(block_pos), _addr(q), _addr(q_pos), q.shape[2], block_list.shape[1], sink_blocks,
+           recent_blocks, _addr(block_list), _addr(block_count), _addr(workspace), _nbytes(workspace), _addr(d_status)),
+          (("bounds", bounds), ("block_pos", block_pos), ("q", q), ("q_pos", q_pos), ("block_list", block_list),
+           ("block_count", block_count), ("workspace", workspace), ("d_status", d_status)), stream)
+
+
+def kvc_block_attention_workspace_bytes(rows: int, group: int, head_dim: int) -> int:
+    return int(lib().kvc_block_attention_workspace_bytes(rows, group, head_dim))
+
+
+def kvc_block_attention(cache: Cache, q: torch.Tensor, q_pos: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+                        workspace: torch.Tensor, block_list: Optional[torch.Tensor] = None,
+                        block_count: Optional[torch.Tensor] = None, d_status=None, stream=None):
+    """Attention of one new token over the listed pages (block_list [rows][stride] int32 ascending, block_count [rows]
+    int32), or over the whole rows without a list.  q: [S][L][Hq][D] in the cache dtype; q_pos: [S] int32; out:
+    [S][L][Hq][D] fp32; lse: [S][L][Hq] fp32."""
+    S, L, D = cache.num_seqs, cache.num_layers, cache.k_pool.shape[2]
+    _expect(q, "q", (S, L, None, D), cache.k_pool.dtype)
+    Hq = q.shape[2]
+    _expect(q_pos, "q_pos", (S,), torch.int32)
+    _expect(out, "out", (S, L, Hq, D), torch.float32)
+    _expect(lse, "lse", (S, L, Hq), torch.float32)
+    if (block_list is None) != (block_count is None):
+        raise KvcError("block_list and block_count go together")
+    if block_list is not None:
+        _expect(block_list, "block_list", (cache.rows, None), torch.int32)
+        _expect(block_count, "block_count", (cache.rows,), torch.int32)
+    _call("kvc_block_attention", cache,
+          (_addr(q), _addr(q_pos), Hq, _addr(block_list), 0 if block_list is None else block_list.shape[1],
+           _addr(block_count), _addr(out), _addr(lse), _addr(workspace), _nbytes(workspace), _addr(d_status)),
+          (("q", q), ("q_pos", q_pos), ("out", out), ("lse", lse), ("workspace", workspace), ("block_list", block_list),
+           ("block_count", block_count), ("d_status", d_status)), stream)
 
 
 def ratchet_seq_states(state: torch.Tensor, num_seqs: int):

@@ -27,6 +27,15 @@
  *      kvc_beacon_update       beacon queries kept by online k-means over each
  *                              group's past queries ("BeaconKV", Key ideas)
  *
+ * Next to the path, one model step over the cache (its attention may read the whole row or only
+ * the pages that a cheap score chooses):
+ *      kvc_reserve_slots       pages, block-table entries and slot maps for the requests' new tokens
+ *      kvc_norm_rope_write     per-head norms and position rotation of queries and keys, keys and
+ *                              values written into the reserved slots
+ *      kvc_block_bounds        per-page minimum and maximum of the keys
+ *      kvc_select_blocks       the pages with the highest bound on the query's logits
+ *      kvc_block_attention     attention of one new token over those pages, or over the row
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  * - Every pointer inside the structures and every array argument is DEVICE memory
@@ -81,6 +90,7 @@ typedef enum {
 #define KVC_DEV_BAD_MOVE 6       /* a move outside [0, row_len) or not hole/survivor */
 #define KVC_DEV_TIMEOUT 7        /* a bounded wait inside a kernel gave up */
 #define KVC_DEV_BAD_STEPS 8      /* step table not ascending from 0, num_steps out of range, or a negative position */
+#define KVC_DEV_BAD_LIST 9       /* block list not ascending, or an entry or its count outside the row */
 
 typedef enum { KVC_F32 = 0, KVC_BF16 = 1 } kvc_dtype;
 
@@ -139,6 +149,9 @@ typedef struct {
 #define KVC_SCORE_ACCUMULATE 1u  /* add into scores instead of overwriting them */
 #define KVC_SCORE_COMPUTE_LSE 2u /* run kvc_query_lse first (beacons have no decode-time LSE) */
 #define KVC_SCORE_SIMT 4u        /* force the CUDA-core path even for bf16 (cross-check) */
+
+/* flags of kvc_norm_rope_write */
+#define KVC_ROPE_INTERLEAVED 1u /* rotate the pairs (2j, 2j + 1) instead of (j, j + rope_dim / 2) */
 
 /* flags of kvc_lrfu_update */
 #define KVC_HIT_BINARY 1u /* a hit counts 1 instead of its attention score */
@@ -323,6 +336,135 @@ size_t kvc_append_workspace_bytes(int32_t rows);
 kvc_status kvc_append_tokens(const kvc_cache *cache, const void *k_new, const void *v_new, const int32_t *new_pos,
                              int32_t count, uint8_t label, float *crf, int32_t *free_pages, int64_t *free_count,
                              void *workspace, size_t workspace_bytes, int32_t *d_status, kvc_stream_t stream);
+
+/* bytes of device workspace kvc_reserve_slots needs for `rows` rows */
+size_t kvc_reserve_workspace_bytes(int32_t rows);
+
+/*
+ * Slots for the new tokens of a step, from the requests' lengths: sequence s brings new_count[s] tokens (0 to
+ * many), packed one sequence after another, and token i of sequence s goes to slot row_len + i of each of the
+ * sequence's rows, whatever length each row has.  Where a row reaches a logical page it does not hold, it takes
+ * one from the top of the free-page stack, in the order of kvc_append_tokens: row r's k-th new page is
+ * free_pages[depth - total + offset_r + k], offset_r the pages all lower rows take, total the pages of the call.
+ * In:   new_count, next_pos [num_seqs] int32 (next_pos: the position of the sequence's first new token);
+ *       free_pages, free_count (device int64: the stack's depth); max_tokens: the size of token_pos and slot_map.
+ * Out:  token_start  [num_seqs + 1] int32: where each sequence's tokens begin, and the number of tokens.
+ *       token_pos    [max_tokens] int32: each token's position (-1 past the last token).
+ *       slot_map     [max_tokens][num_layers][num_kv_heads] int64: page * page_size + offset of the token's
+ *                    slot in each of its sequence's rows, -1 past the last token and for refused rows.
+ *       row_len_out  [rows] int32: the new lengths; may be cache->row_len itself.
+ *       free_count_out  device int64: the new depth; may be free_count itself.
+ * In/out: the cache's block_table (entries of new pages), slot_pos and slot_label (`label`), and crf
+ *       ([rows][max_slots] fp32, may be NULL; 0) of the new slots.  k_pool and v_pool are not touched.
+ * Device faults: more than max_tokens tokens (KVC_DEV_BAD_LENGTH, row -1) or a stack too shallow
+ * (KVC_DEV_FREED_OVERFLOW, row -1) reserve nothing: row_len_out and free_count_out get the old values and the slot
+ * map -1 throughout.  A row is left alone and its slots are -1 when it would exceed max_slots
+ * (KVC_DEV_FREED_OVERFLOW), its length is out of range or its positions would leave [0, INT32_MAX)
+ * (KVC_DEV_BAD_LENGTH), or the page its first new token joins is bad (KVC_DEV_BAD_PAGE).  A negative count is
+ * reported (KVC_DEV_BAD_LENGTH) and counts as 0.  A page id on the stack outside the pool is reported
+ * (KVC_DEV_BAD_PAGE) and its tokens' slots are -1, but the row has taken it.
+ * workspace: kvc_reserve_workspace_bytes(rows) bytes; its contents need not be kept between calls.
+ */
+kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, const int32_t *next_pos, uint8_t label,
+                             float *crf, const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
+                             int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                             int64_t *slot_map, void *workspace, size_t workspace_bytes, int32_t *d_status,
+                             kvc_stream_t stream);
+
+/*
+ * Queries and keys of a step normalised for each head and rotated by their positions, and keys and values
+ * written into the cache, in one pass.  For every head vector x of a query or key:
+ *     y = x * w / sqrt(mean(x^2) + eps)                        (w: q_weight or k_weight; y = x where it is NULL)
+ * and, over the first rope_dim elements, with f_j = token_pos * inv_freq[j], j < rope_dim / 2,
+ *     (y_a, y_b) <- (y_a cos f_j - y_b sin f_j, y_a sin f_j + y_b cos f_j)
+ * for (a, b) = (j, j + rope_dim / 2), or (2 j, 2 j + 1) with KVC_ROPE_INTERLEAVED.  Values are copied.  The
+ * arithmetic is fp32 with one rounding at the end; the angle is taken in 64 bits, so far positions keep theirs.
+ * qkv:       [num_tokens] tokens, token_stride elements apart, of [num_layers][num_q_heads + 2 * num_kv_heads]
+ *            [head_dim] in the cache's dtype: query heads, then key heads, then value heads.  16-byte aligned,
+ *            token_stride a multiple of 16 bytes.
+ * token_count: NULL, or a device int32: only the first min(*token_count, num_tokens) tokens are present (for
+ *            instance token_start + num_seqs of kvc_reserve_slots).
+ * q_weight, k_weight: NULL or [num_layers][head_dim] in the cache's dtype, 16-byte aligned.
+ * inv_freq:  [rope_dim / 2] fp32; rope_dim a multiple of 16 up to head_dim, 0 for no rotation.
+ * token_pos: [num_tokens] int32.
+ * slot_map:  [num_tokens][num_layers][num_kv_heads] int64 physical slots (page * page_size + offset).  -1 writes no
+ *            key and value; one outside the pool does not either and is reported (KVC_DEV_BAD_PAGE, row -1).  No two
+ *            entries may name the same slot.
+ * q_out:     [num_tokens][num_layers][num_q_heads][head_dim] in the cache's dtype, 16-byte aligned; tokens that are
+ *            not present are left as they were.  May not overlap qkv.
+ * Of the cache only the pools and sizes are used (num_seqs is not).
+ */
+kvc_status kvc_norm_rope_write(const kvc_cache *cache, const void *qkv, int64_t token_stride, int32_t num_tokens,
+                               const int32_t *token_count, int32_t num_q_heads, const void *q_weight,
+                               const void *k_weight, float eps, const float *inv_freq, int32_t rope_dim, uint32_t flags,
+                               const int32_t *token_pos, const int64_t *slot_map, void *q_out, int32_t *d_status,
+                               kvc_stream_t stream);
+
+/*
+ * Bounds of every page's keys: over the row's slots in page b,
+ *     bounds[row][b][0][d] = min k[d],   bounds[row][b][1][d] = max k[d],   block_pos[row][b] = min slot_pos.
+ * bounds:    [rows][max_pages_per_row][2][head_dim] in the cache's dtype (exact), 16-byte aligned.  An element with a
+ *            NaN among its keys is NaN.
+ * block_pos: [rows][max_pages_per_row] int32.
+ * from_len:  NULL for all pages, or [rows] int32: only the pages from the one that holds slot from_len[row] on
+ *            are brought up to date (the row's length before an append); a compaction moves entries anywhere, so
+ *            after it all pages are.
+ * Written for the pages that hold slots below row_len; the others are left as they were.  A page id outside
+ * the pool is reported (KVC_DEV_BAD_PAGE): its bounds are not written and its block_pos is INT32_MAX.
+ */
+kvc_status kvc_block_bounds(const kvc_cache *cache, const int32_t *from_len, void *bounds, int32_t *block_pos,
+                            int32_t *d_status, kvc_stream_t stream);
+
+/* bytes of device workspace kvc_select_blocks needs */
+size_t kvc_select_blocks_workspace_bytes(int32_t rows, int32_t max_pages_per_row);
+
+/*
+ * The pages a decode query attends to.  With the bounds of kvc_block_bounds, no key of page b has a larger sum of the
+ * group's logits than
+ *     score_b = sum_g sum_d max(q_gd * lo_bd, q_gd * hi_bd)     (times 1 / sqrt(head_dim), which orders nothing)
+ * over the query heads g of the row's group.  Of the pages that hold slots below row_len and are visible
+ * (block_pos <= q_pos), the row's first sink_blocks and last recent_blocks pages are always taken, and the rest of
+ * top_k goes to the highest scores, ties to the lower page index; a page whose bounds are not
+ * finite, or whose score is NaN, ranks with +inf (so that attention shows such keys instead of passing over them).  The scores are taken in 64 bits, so the choice does not depend on the order of a sum.
+ * bounds, block_pos: as kvc_block_bounds writes them.  q, q_pos: as for kvc_decode_attention.
+ * top_k:       at least 1; sink_blocks + recent_blocks may not exceed it.
+ * block_list:  [rows][top_k] int32: logical page indexes, ascending, then -1.
+ * block_count: [rows] int32: min(top_k, the row's visible pages).  A row whose length is out of range is
+ *              reported and gets 0.
+ * workspace:   kvc_select_blocks_workspace_bytes(rows, max_pages_per_row) bytes; contents need not be kept.
+ * At most 128 query heads per KV head.
+ */
+kvc_status kvc_select_blocks(const kvc_cache *cache, const void *bounds, const int32_t *block_pos, const void *q,
+                             const int32_t *q_pos, int32_t num_q_heads, int32_t top_k, int32_t sink_blocks,
+                             int32_t recent_blocks, int32_t *block_list, int32_t *block_count, void *workspace,
+                             size_t workspace_bytes, int32_t *d_status, kvc_stream_t stream);
+
+/* bytes of device workspace kvc_block_attention needs on the current device; group = num_q_heads / num_kv_heads */
+size_t kvc_block_attention_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim);
+
+/*
+ * Attention of one new token over the listed pages of each row, or over the whole row: out and lse as for
+ * kvc_decode_attention (same q, q_pos and masking by slot_pos), over the slots below row_len of the pages
+ * block_list[row][0 .. block_count[row] - 1].  No scores are kept, so rows may have any length, and the work is split evenly
+ * over the GPU whatever the number of rows and their lengths.
+ * block_list:  [rows][list_stride] int32 logical pages, strictly ascending (kvc_select_blocks' list with list_stride =
+ *              top_k), or NULL for all pages (list_stride and block_count are then not used).
+ * block_count: [rows] int32 in [0, list_stride].
+ * out:         [num_seqs][num_layers][num_q_heads][head_dim] fp32; lse: [num_seqs][num_layers][num_q_heads] fp32.
+ *              A row with no visible slot gets zeros and -inf.  Hidden slots may hold any bits; a visible key or
+ *              value that is not finite leaves the outputs it reaches not finite or undefined.
+ * workspace:   kvc_block_attention_workspace_bytes(rows, group, head_dim) bytes; contents need not be kept.  Calls
+ *              that may overlap on the GPU need workspaces of their own.
+ * Limits:      num_q_heads / num_kv_heads <= 8.
+ * Device faults: KVC_DEV_BAD_LENGTH, or KVC_DEV_BAD_LIST for a count or last entry outside the row: the row's results are
+ * those of no visible slot.  KVC_DEV_BAD_LIST for another entry that is out of range or not ascending, or
+ * KVC_DEV_BAD_PAGE: that page is left out.
+ * Every sum runs in a fixed order: results repeat bit for bit on the same device.
+ */
+kvc_status kvc_block_attention(const kvc_cache *cache, const void *q, const int32_t *q_pos, int32_t num_q_heads,
+                               const int32_t *block_list, int32_t list_stride, const int32_t *block_count, float *out,
+                               float *lse, void *workspace, size_t workspace_bytes, int32_t *d_status,
+                               kvc_stream_t stream);
 
 /* bytes of the ratchet state buffer for num_seqs sequences */
 size_t kvc_ratchet_state_bytes(int32_t num_seqs, const kvc_ratchet_params *params);
