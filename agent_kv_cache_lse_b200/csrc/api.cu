@@ -466,7 +466,8 @@ kvc_status kvc_select_blocks(const kvc_cache *cache, const void *bounds, const i
 }
 
 size_t kvc_block_attention_workspace_bytes(int32_t rows, int32_t group, int32_t head_dim) {
-    return rows < 0 || group <= 0 || head_dim <= 0 ? 0 : kvc::block_attention_workspace(rows, group, head_dim);
+    // the parts are the CTAs', whatever the rows
+    return rows < 0 || group <= 0 || head_dim <= 0 ? 0 : kvc::block_attention_workspace(group, head_dim);
 }
 
 kvc_status kvc_block_attention(const kvc_cache *cache, const void *q, const int32_t *q_pos, int32_t num_q_heads,
@@ -484,7 +485,7 @@ kvc_status kvc_block_attention(const kvc_cache *cache, const void *q, const int3
     if (group > 8) return fail(KVC_ERR_UNSUPPORTED, "at most 8 query heads per KV head");
     if (block_list && (!block_count || list_stride <= 0))
         return fail(KVC_ERR_INVALID_ARGUMENT, "a block list needs block_count and a positive list_stride");
-    const size_t need = kvc::block_attention_workspace(c.rows, group, c.head_dim);
+    const size_t need = kvc::block_attention_workspace(group, c.head_dim);
     if (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 7))
         return fail(KVC_ERR_INVALID_ARGUMENT, "workspace must be 8-byte aligned and at least %zu bytes", need);
     return cuda_status(kvc::launch_block_attention(c, q, q_pos, num_q_heads, block_list, list_stride, block_count, out,

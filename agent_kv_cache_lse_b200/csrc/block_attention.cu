@@ -6,22 +6,21 @@
 //     l[g, i] = q_g . k_i / sqrt(D),  lse[g] = log sum_i exp(l[g, i]),  out[g] = sum_i exp(l[g, i] - lse[g]) v_i.
 // K and V are read once and nothing of size [heads][slots] is kept, so a row may have any length.
 //
-// The split.  A row's slots, in list order, are cut into chunks of CH (16 at bf16, 8 at fp32); the chunks of all rows, one
-// row after another, form one sequence of U chunks, and W warps of the launch take equal runs
-// [U w / W, U (w + 1) / W) of it, wherever rows begin and end.  So the load is even whether there are a few long rows, many
-// short ones or rows of unlike lengths, and no warp waits for another.  Every CTA sums the rows' chunk counts
-// (from row_len, or the list's length) to find where its warps start.
-//
-// A warp streams its chunks' K and V rows through a ring of kRing stages of its own with 16-byte cp.async, kRing - 1
-// chunks ahead, keeps a running maximum m, sum s and output o for each head (online softmax), and at the end of its run or of
-// a row leaves (m, s, o) as a part in the workspace.  Parts are numbered w + row: along the sequence each new part has a new
-// warp or a new row, never both old, so the number is unique and a row's parts are consecutive.  A second launch joins each
-// (row, head): M = max m_j, out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) s_j, in the order of the parts, so results
-// repeat bit for bit.
+// The split.  A row's slots, in list order, are cut into chunks of CH (16 at bf16, 8 at fp32), and the chunks of all
+// rows are shared out evenly over the launch's warps (rowshare.cuh).  A warp streams its run's K and V rows through a ring of
+// kRing stages of its own with 16-byte cp.async, kRing - 1 chunks ahead, and keeps a running maximum m, sum s and output o
+// for each head (online softmax).  A row that lies inside one run is finished by its warp.  The parts (m, s, o) of one
+// that does not are joined within the CTA through shared memory, and if the row goes on in other CTAs, the CTA leaves one
+// part in the workspace: slot 1 of the CTA where the row begins, slot 0 of the others.  A second launch, which is
+// resident before the first ends (programmatic dependent launch), joins those: M = max m_j,
+// out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) s_j.  All joins are in the order of the sequence, so results repeat
+// bit for bit.
 //
 // bf16: the chunk's two contractions are warp-level tensor-core tiles (m16n8k16, fp32 accumulate), S = K Q^T with the 16 keys
 // as rows and the heads (padded to 8) as columns, O^T += V^T P with D as rows.  P is split into three bf16 parts whose sum
 // keeps 24 bits, all of fp32's: two parts (16 bits) left the fp32 output 5e-6 off where the plain form is 4e-7 off.
+// A tensor-core step truncates when it adds to its accumulator, which over a run of hundreds of chunks drifts (7e-6 at 138
+// chunks), so each chunk's product starts from zero and is added to the run's output by a rounded fp32 addition.
 // fp32: a lane owns 8 elements of D of a key and all dot products are fp32 FMAs.
 #include <cuda_bf16.h>
 
@@ -30,6 +29,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "rowshare.cuh"
 
 namespace kvc {
 namespace {
@@ -38,8 +38,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRing = 3;       // stages a warp
 constexpr int kMinRun = 2;     // chunks a run, where there are that many
+constexpr int kMaxGroup = 8;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 
 struct AttnArgs {
     CacheView c;
@@ -50,9 +51,8 @@ struct AttnArgs {
     int32_t list_stride;
     const int32_t *list_len;
     float *out, *lse;
-    float *parts;          // [W + rows][group * (D + 2)]: o, then m and s of each head
-    int64_t *row_start;    // [rows]: first chunk of the row in the sequence (written where the row has chunks)
-    int64_t *total;        // U
+    float *parts;          // [CTAs][2][group * (D + 2)]: o, then m and s of each head
+    int2 *spans;           // [CTAs]: the row that begins in the CTA and goes on after it (-1: none), and its last CTA
     float scale_log2;      // log2(e) / sqrt(D)
     int32_t *status;
 };
@@ -127,20 +127,9 @@ __device__ __forceinline__ int row_slots(const AttnArgs &a, int r, bool tell) {
     return k * P - (last == nb - 1 ? nb * P - n : 0);  // only the row's last page may be partly filled
 }
 
-// How U chunks are shared out: `per_cta` warps of each CTA take runs, W in all, every run at least one chunk (kMinRun where
-// U allows it, so that a short launch does not spread into parts that cost more to join than to stream).
-struct Share {
-    int per_cta, W;
-};
-__device__ __forceinline__ Share share_of(int64_t U, int ctas) {
-    const int64_t per = U / ((int64_t)ctas * kMinRun);
-    Share s;
-    s.per_cta = (int)(per < 1 ? 1 : per > kWarps ? kWarps : per);
-    s.W = (int)min(U, (int64_t)ctas * s.per_cta);
-    return s;
-}
-// first chunk of run w
-__device__ __forceinline__ int64_t run_start(int64_t U, int w, int W) { return U * w / W; }
+// out and lse of one (row, head) from a sum of weights and the weighted sum of V elements
+__device__ __forceinline__ float ratio(float acc, float sum) { return sum == 0.f ? 0.f : acc / sum; }
+__device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
 
 template <typename T, int D, int GM, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
@@ -154,70 +143,40 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     constexpr int LK = D / 8, KW = 32 / LK, STEPS = CH / KW;  // fp32: lanes a key, keys a step
     constexpr float kSlack = 8.f;                     // bf16: the maximum moves only when a logit passes it by 8 (log2)
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ long long scan_s[kWarps];
-    __shared__ int start_row[kWarps];
-    __shared__ long long start_off[kWarps];
+    __shared__ RunTable<kWarps> runs;
+    __shared__ int4 segs[2 * kWarps];  // parts left in shared memory, in order: row (-1: none), begins here, ends here,
+                                       // chunks the row has after the run
     const CacheView &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int G = a.group, Hkv = c.num_kv_heads, P = c.page_size;
-
-    // where the warps' runs start: each thread sums the chunks of its share of the rows, the CTA scans the sums
-    int64_t U = 0;
-    {
-        const int share = (c.rows + kThreads - 1) / kThreads;
-        const int r0 = min(c.rows, tid * share), r1 = min(c.rows, r0 + share);
-        long long mine = 0;
-        for (int r = r0; r < r1; ++r) mine += (row_slots(a, r, blockIdx.x == 0) + CH - 1) / CH;
-        long long x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+    const int G = a.group, Hkv = c.num_kv_heads, P = c.page_size, rec = G * (D + 2);
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (tid < 2 * kWarps) segs[tid] = make_int4(-1, 0, 0, 0);
+    if (tid == 0) a.spans[blockIdx.x] = make_int2(-1, 0);
+    const Share sh = share_rows<kWarps>(c.rows, kMinRun, runs, [&](int r) {
+        return (row_slots(a, r, blockIdx.x == 0) + CH - 1) / CH;
+    });
+    // rows without slots are answered here, a thread a row to look and a warp a row to write
+    for (int r0 = blockIdx.x * kThreads + warp * 32; r0 < c.rows; r0 += gridDim.x * kThreads) {
+        unsigned empty = __ballot_sync(0xffffffffu, r0 + lane < c.rows && row_slots(a, r0 + lane, false) == 0);
+        for (; empty; empty &= empty - 1) {
+            const int r = r0 + __ffs(empty) - 1;
+            const int64_t head = (int64_t)(r / Hkv) * a.num_q_heads + (r % Hkv) * G;
+            for (int e = lane; e < G * D; e += 32) a.out[head * D + e] = 0.f;
+            if (lane < G) a.lse[head + lane] = -INFINITY;
         }
-        if (lane == 31) scan_s[warp] = x;
-        if (tid < kWarps) start_row[tid] = c.rows, start_off[tid] = 0;
-        __syncthreads();
-        long long before = x - mine;
-        for (int k = 0; k < kWarps; ++k) {
-            if (k < warp) before += scan_s[k];
-            U += scan_s[k];
-        }
-        const Share sh = share_of(U, gridDim.x);
-        for (int k = 0; k < sh.per_cta && blockIdx.x * sh.per_cta + k < sh.W; ++k) {
-            const int64_t s = run_start(U, blockIdx.x * sh.per_cta + k, sh.W);
-            if (s >= before && s < before + mine) {  // the run starts in one of this thread's rows
-                int64_t at = before;
-                for (int r = r0; r < r1; ++r) {
-                    const int nch = (row_slots(a, r, false) + CH - 1) / CH;
-                    if (s < at + nch) {
-                        start_row[k] = r;
-                        start_off[k] = s - at;
-                        break;
-                    }
-                    at += nch;
-                }
-            }
-        }
-        if (blockIdx.x == 0) {  // the join looks rows up in the sequence
-            int64_t at = before;
-            for (int r = r0; r < r1; ++r) {
-                a.row_start[r] = at;
-                at += (row_slots(a, r, false) + CH - 1) / CH;
-            }
-            if (tid == 0) *a.total = U;
-        }
-        __syncthreads();
     }
 
     unsigned char *ring = smem + (size_t)warp * kRing * kStage;
     const T *kp = static_cast<const T *>(c.k_pool);
     const T *vp = static_cast<const T *>(c.v_pool);
-    const Share sh = share_of(U, gridDim.x);
+    // where a run's first part goes when its row ends in the run but began before it; its last part goes to the warp's
+    // own ring, which is free by then
+    float *head_part = reinterpret_cast<float *>(smem + (size_t)kWarps * kRing * kStage) + warp * rec;
     const int w = blockIdx.x * sh.per_cta + warp;
-    if (warp >= sh.per_cta || w >= sh.W) return;
-    int64_t left = run_start(U, w + 1, sh.W) - run_start(U, w, sh.W);
-    int off = (int)start_off[warp];
-    for (int row = start_row[warp]; left > 0; ++row, off = 0) {
+    const bool works = warp < sh.per_cta && w < sh.W;
+    int64_t left = works ? run_start(sh, w + 1) - run_start(sh, w) : 0;
+    int off = works ? runs.off[warp] : 0;
+    for (int row = works ? runs.row[warp] : 0; left > 0; ++row, off = 0) {
         const int slots = row_slots(a, row, false);
         const int nch = (slots + CH - 1) / CH;
         const int cnt = (int)min((int64_t)(nch - off), left);
@@ -440,8 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
                     for (int t = 0; t < NS; ++t) {
                         uint32_t af[4];
                         ldsm_x4_t(rowa + ((((uint32_t)(2 * t + ((lane >> 3) & 1))) ^ (key & 7)) << 4), af);
+                        float pv[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int x = 0; x < 3; ++x) mma16816(oc[t], af, pa[x], pb[x]);
+                        for (int x = 0; x < 3; ++x) mma16816(pv, af, pa[x], pb[x]);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) oc[t][u] += pv[u];
                     }
                 }
             } else {
@@ -501,8 +463,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
         if (bad_page) report(a.status, KVC_DEV_BAD_PAGE, row);
         if (bad_list) report(a.status, KVC_DEV_BAD_LIST, row);
 
-        // the part
-        float *part = a.parts + (int64_t)(w + row) * G * (D + 2), *stat = part + G * D;
+        // the row's result, or its part
+        const bool begins = off == 0, ends = off + cnt == nch, whole = begins && ends;
+        float *part = whole ? a.out + hbase * D : ends ? head_part : reinterpret_cast<float *>(ring);
+        float *stat = part + G * D;
+        if (!whole && lane == 0) segs[2 * warp + (ends ? 0 : 1)] = make_int4(row, begins, ends, nch - off - cnt);
         if constexpr (MM) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
@@ -514,13 +479,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
             for (int u = 0; u < 2; ++u)
                 if (hm + u < G) {
                     if (lane < 4) {
-                        stat[2 * (hm + u)] = mm[u];
-                        stat[2 * (hm + u) + 1] = ms[u];
+                        if (whole) {
+                            a.lse[hbase + hm + u] = log_sum(mm[u], ms[u]);
+                        } else {
+                            stat[2 * (hm + u)] = mm[u];
+                            stat[2 * (hm + u) + 1] = ms[u];
+                        }
                     }
+                    const float div = whole ? ms[u] : 1.f;
 #pragma unroll
                     for (int t = 0; t < NS; ++t) {
-                        part[(hm + u) * D + 16 * t + (lane >> 2)] = oc[t][u];
-                        part[(hm + u) * D + 16 * t + (lane >> 2) + 8] = oc[t][2 + u];
+                        part[(hm + u) * D + 16 * t + (lane >> 2)] = ratio(oc[t][u], div);
+                        part[(hm + u) * D + 16 * t + (lane >> 2) + 8] = ratio(oc[t][2 + u], div);
                     }
                 }
         } else {
@@ -533,108 +503,164 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u) o[g][u] += __shfl_xor_sync(0xffffffffu, o[g][u], x);
                     }
-                    if (lane == 0) stat[2 * g] = m[g], stat[2 * g + 1] = s[g];
-                    if (kslot == 0) {
-                        *reinterpret_cast<float2 *>(part + g * D + d0) = make_float2(o[g][0], o[g][1]);
-                        *reinterpret_cast<float2 *>(part + g * D + d0 + 2) = make_float2(o[g][2], o[g][3]);
-                        *reinterpret_cast<float2 *>(part + g * D + D / 2 + d0) = make_float2(o[g][4], o[g][5]);
-                        *reinterpret_cast<float2 *>(part + g * D + D / 2 + d0 + 2) = make_float2(o[g][6], o[g][7]);
+                    if (lane == 0) {
+                        if (whole) a.lse[hbase + g] = log_sum(m[g], s[g]);
+                        else stat[2 * g] = m[g], stat[2 * g + 1] = s[g];
                     }
+                    const float div = whole ? s[g] : 1.f;
+                    if (kslot == 0)
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) part[g * D + (u >> 2) * (D / 2) + d0 + (u & 3)] = ratio(o[g][u], div);
                 }
             }
         }
         __syncwarp();
     }
+    __syncthreads();
+
+    // join the parts of each row the CTA shares
+    for (int i = 0; i < 2 * kWarps;) {
+        const int row = segs[i].x;
+        if (row < 0) {
+            ++i;
+            continue;
+        }
+        int j = i;  // the row's last part in this CTA
+        for (int k = i + 1; k < 2 * kWarps; ++k)
+            if (segs[k].x == row) j = k;
+        const bool begins = segs[i].y, ends = segs[j].z, whole = begins && ends;
+        const int64_t hbase = (int64_t)(row / Hkv) * a.num_q_heads + (row % Hkv) * G;
+        float *part = whole ? a.out + hbase * D : a.parts + (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * rec;
+        auto seg = [&](int k) {
+            return reinterpret_cast<const float *>(smem + ((k & 1) ? (size_t)(k >> 1) * kRing * kStage
+                                                                   : (size_t)kWarps * kRing * kStage + (size_t)(k >> 1) * rec * 4));
+        };
+        for (int e = tid; e < G * D; e += kThreads) {
+            const int g = e / D;
+            float M = -INFINITY, acc = 0.f, sum = 0.f;
+            for (int k = i; k <= j; ++k)
+                if (segs[k].x == row) M = fmaxf(M, seg(k)[G * D + 2 * g]);
+            for (int k = i; k <= j; ++k)
+                if (segs[k].x == row) {
+                    const float f = weight(seg(k)[G * D + 2 * g], M);
+                    sum += f * seg(k)[G * D + 2 * g + 1];
+                    acc += f * seg(k)[e];
+                }
+            part[e] = whole ? ratio(acc, sum) : acc;
+            if (e == g * D) {
+                if (whole) a.lse[hbase + g] = log_sum(M, sum);
+                else part[G * D + 2 * g] = M, part[G * D + 2 * g + 1] = sum;
+            }
+        }
+        if (begins && !ends && tid == 0) {  // the CTA's last row: where does it end?
+            const int64_t next = run_start(sh, min(sh.W, (int)(blockIdx.x + 1) * sh.per_cta));
+            a.spans[blockIdx.x] = make_int2(row, run_of(sh, next + segs[j].w - 1) / sh.per_cta);
+        }
+        i = j + 1;
+    }
 }
 
-// One CTA a (row, head): kJoinThreads / D threads an element of the output, each over every such part of the row's
+// Joins the parts of a row that lies in several CTAs: a CTA of this launch for each CTA of the first (the one where the
+// row begins) and head; four elements a thread, and threads of one element take every SL-th part each.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, int ctas, int CH) {
-    constexpr int SL = kJoinThreads / D;
-    __shared__ float red[32];
-    __shared__ float acc_s[SL][D];
-    const CacheView &c = a.c;
-    const int row = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, G = a.group;
-    const int64_t head = (int64_t)(row / c.num_kv_heads) * a.num_q_heads + (row % c.num_kv_heads) * G + g;
-    const int nch = (row_slots(a, row, false) + CH - 1) / CH;
-    float *out = a.out + head * D;
-    if (nch == 0) {
-        for (int d = tid; d < D; d += kJoinThreads) out[d] = 0.f;
-        if (tid == 0) a.lse[head] = -INFINITY;
-        return;
-    }
-    const int64_t U = *a.total, x0 = a.row_start[row], x1 = x0 + nch - 1;
-    const int W = share_of(U, ctas).W;
-    // run of chunk x: the last w with U w / W <= x
-    const int w0 = (int)(((x0 + 1) * W - 1) / U), w1 = (int)(((x1 + 1) * W - 1) / U);
-    const int64_t rec = (int64_t)G * (D + 2);
-    const float *part = a.parts + (int64_t)(w0 + row) * rec;
-    const int np = w1 - w0 + 1;
-    float mx = -INFINITY;
-    for (int j = tid; j < np; j += kJoinThreads) mx = fmaxf(mx, part[j * rec + G * D + 2 * g]);
-    const float M = block_max(mx, red);
-    const int d = tid % D, sl = tid / D;
-    float acc = 0.f, sum = 0.f;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
+    constexpr int LANES = D / 4, SL = kJoinThreads / LANES;
+    __shared__ float4 acc_s[SL][LANES];
+    __shared__ float sum_s[SL];
+    const int first = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, G = a.group, rec = G * (D + 2);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 span = a.spans[first];
+    const int row = span.x, np = span.y - first + 1;
+    if (row < 0) return;
+    const int64_t head = (int64_t)(row / a.c.num_kv_heads) * a.num_q_heads + (row % a.c.num_kv_heads) * G + g;
+    auto part = [&](int j) { return a.parts + (int64_t)(2 * (first + j) + (j == 0 ? 1 : 0)) * rec; };
+    float M = -INFINITY;  // every warp finds it for itself
+    for (int j = lane; j < np; j += 32) M = fmaxf(M, part(j)[G * D + 2 * g]);
+    M = warp_max(M);
+    const int d = tid % LANES, sl = tid / LANES;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
     for (int j = sl; j < np; j += SL) {
-        const float f = weight(part[j * rec + G * D + 2 * g], M);
-        sum += f * part[j * rec + G * D + 2 * g + 1];
-        acc += f * part[j * rec + g * D + d];
+        const float *p = part(j);
+        const float2 ms = *reinterpret_cast<const float2 *>(p + G * D + 2 * g);
+        const float2 x = reinterpret_cast<const float2 *>(p + g * D)[2 * d], y = reinterpret_cast<const float2 *>(p + g * D)[2 * d + 1];
+        const float f = weight(ms.x, M);
+        sum += f * ms.y;
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * y.x;
+        acc.w += f * y.y;
     }
     acc_s[sl][d] = acc;
-    __shared__ float sum_s[SL];
     if (d == 0) sum_s[sl] = sum;
     __syncthreads();
     if (sl == 0) {
-        acc = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
         sum = 0.f;
         for (int k = 0; k < SL; ++k) {
-            acc += acc_s[k][d];
+            acc.x += acc_s[k][d].x;
+            acc.y += acc_s[k][d].y;
+            acc.z += acc_s[k][d].z;
+            acc.w += acc_s[k][d].w;
             sum += sum_s[k];
         }
-        out[d] = sum > 0.f ? acc / sum : (sum == 0.f ? 0.f : sum);
-        if (d == 0) a.lse[head] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * kLn2;
+        float *out = a.out + head * D + 4 * d;
+        out[0] = ratio(acc.x, sum);
+        out[1] = ratio(acc.y, sum);
+        out[2] = ratio(acc.z, sum);
+        out[3] = ratio(acc.w, sum);
+        if (d == 0) a.lse[head] = log_sum(M, sum);
     }
 }
 
 template <typename T, int D, int GM>
 cudaError_t launch_main(const AttnArgs &a, int grid, cudaStream_t stream) {
     constexpr int CH = sizeof(T) == 2 ? 16 : 8;
-    constexpr size_t kSmem = (size_t)kWarps * kRing * (2 * CH * D * sizeof(T) + CH * 4);
-    static_assert(kSmem <= 226 * 1024, "shared memory");
+    constexpr size_t kRings = (size_t)kWarps * kRing * (2 * CH * D * sizeof(T) + CH * 4);
+    static_assert(kRings + kWarps * kMaxGroup * (D + 2) * 4 <= 226 * 1024, "shared memory");
+    const size_t bytes = kRings + (size_t)kWarps * a.group * (D + 2) * 4;
     const bool whole = a.c.page_size % CH == 0;
     auto kernel = whole ? attention_kernel<T, D, GM, true> : attention_kernel<T, D, GM, false>;
     static int done[2][kMaxDevices];
-    cudaError_t e = dyn_smem_at_least(reinterpret_cast<const void *>(kernel), kSmem, done[whole]);
+    cudaError_t e = dyn_smem_at_least(reinterpret_cast<const void *>(kernel), bytes, done[whole]);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmem, stream>>>(a);
+    kernel<<<grid, kThreads, bytes, stream>>>(a);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch(const AttnArgs &a, int grid, cudaStream_t stream) {
-    const bool bf16 = a.c.dtype == KVC_BF16;
     cudaError_t e;
-    if (bf16) e = launch_main<__nv_bfloat16, D, 8>(a, grid, stream);
+    if (a.c.dtype == KVC_BF16) e = launch_main<__nv_bfloat16, D, 8>(a, grid, stream);
     else if (a.group == 1) e = launch_main<float, D, 1>(a, grid, stream);
     else if (a.group == 2) e = launch_main<float, D, 2>(a, grid, stream);
     else if (a.group <= 4) e = launch_main<float, D, 4>(a, grid, stream);
     else e = launch_main<float, D, 8>(a, grid, stream);
     if (e != cudaSuccess) return e;
-    join_kernel<D><<<dim3(a.c.rows, a.group), kJoinThreads, 0, stream>>>(a, grid, bf16 ? 16 : 8);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid, a.group);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a);
 }
 
 }  // namespace
 
-size_t block_attention_workspace(int64_t rows, int32_t group, int32_t head_dim) {
-    const int64_t warps = (int64_t)device_sms() * kWarps;
-    const int64_t head = (rows + 1) * (int64_t)sizeof(int64_t);  // row starts, then the total
-    return (size_t)(head + (head & 8) + (warps + rows) * group * (head_dim + 2) * (int64_t)sizeof(float));
+size_t block_attention_workspace(int32_t group, int32_t head_dim) {
+    const size_t ctas = (size_t)device_sms();
+    return ctas * (sizeof(int2) + 2 * (size_t)group * (head_dim + 2) * sizeof(float));
 }
 
 cudaError_t launch_block_attention(const CacheView &c, const void *q, const int32_t *q_pos, int32_t num_q_heads,
                                    const int32_t *list, int32_t list_stride, const int32_t *list_len, float *out,
                                    float *lse, void *ws, int32_t *status, cudaStream_t stream) {
+    const int grid = device_sms();
     AttnArgs a{};
     a.c = c;
     a.q = q;
@@ -646,12 +672,10 @@ cudaError_t launch_block_attention(const CacheView &c, const void *q, const int3
     a.list_len = list_len;
     a.out = out;
     a.lse = lse;
-    a.row_start = static_cast<int64_t *>(ws);
-    a.total = a.row_start + c.rows;
-    a.parts = reinterpret_cast<float *>(a.row_start + (c.rows + 1 + ((c.rows + 1) & 1)));
+    a.spans = static_cast<int2 *>(ws);
+    a.parts = reinterpret_cast<float *>(a.spans + grid);
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)c.head_dim));
     a.status = status;
-    const int grid = device_sms();
     return c.head_dim == 128 ? launch<128>(a, grid, stream) : launch<64>(a, grid, stream);
 }
 

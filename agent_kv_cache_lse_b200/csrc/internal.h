@@ -118,7 +118,7 @@ cudaError_t launch_select_blocks(const CacheView &c, const void *bounds, const i
                                  const int32_t *q_pos, int32_t num_q_heads, int32_t top_k, int32_t sink, int32_t recent,
                                  int32_t *block_list, int32_t *block_count, void *ws, int32_t *status,
                                  cudaStream_t stream);
-size_t block_attention_workspace(int64_t rows, int32_t group, int32_t head_dim);
+size_t block_attention_workspace(int32_t group, int32_t head_dim);
 cudaError_t launch_block_attention(const CacheView &c, const void *q, const int32_t *q_pos, int32_t num_q_heads,
                                    const int32_t *list, int32_t list_stride, const int32_t *list_len, float *out,
                                    float *lse, void *ws, int32_t *status, cudaStream_t stream);

@@ -1,0 +1,89 @@
+// Even shares of ragged rows: the rows' units of work (chunks of slots, pages), one row after another, form one sequence
+// of U units, and W runs of nearly equal length cut it wherever rows begin and end.  A few long rows, many short ones and
+// rows of unlike lengths then load the GPU alike, and no launch shape depends on lengths that only the device knows.
+#pragma once
+
+#include <cstdint>
+
+namespace kvc {
+
+// per_cta runs for each CTA of the launch (consecutive ones), W in all; every run has at least one unit
+struct Share {
+    int64_t U;
+    int per_cta, W;
+};
+
+// first unit of run w
+__device__ __forceinline__ int64_t run_start(const Share &s, int w) { return s.U * w / s.W; }
+
+// run of unit x: the last w with U w / W <= x
+__device__ __forceinline__ int run_of(const Share &s, int64_t x) { return (int)(((x + 1) * s.W - 1) / s.U); }
+
+// A run of at least min_run units where there are that many, and at most kRuns runs a CTA
+template <int kRuns>
+__device__ __forceinline__ Share share_units(int64_t U, int ctas, int min_run) {
+    const int64_t span = (int64_t)ctas * min_run, per = (U + span - 1) / span;
+    Share s;
+    s.U = U;
+    s.per_cta = (int)(per < 1 ? 1 : per > kRuns ? kRuns : per);
+    s.W = (int)min(U, (int64_t)ctas * s.per_cta);
+    return s;
+}
+
+template <int kRuns>
+struct RunTable {
+    long long scan[32];
+    int row[kRuns];     // the run's first row ...
+    int off[kRuns];     // ... and its first unit in that row
+};
+
+// Share out the rows' units, count(r) of them in row r.  Every CTA sums the counts itself (each thread its share of
+// the rows, then a scan over the CTA) and finds where its runs start.  All threads call it; the table is ready on return.
+template <int kRuns, typename Count>
+__device__ __forceinline__ Share share_rows(int rows, int min_run, RunTable<kRuns> &t, Count count) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int each = (rows + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int r0 = min(rows, tid * each), r1 = min(rows, r0 + each);
+    long long mine = 0;
+    int first = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int n = count(r);
+        if (r == r0) first = n;
+        mine += n;
+    }
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) t.scan[warp] = x;
+    __syncthreads();
+    long long before = x - mine;
+    int64_t U = 0;
+    for (int k = 0; k < nw; ++k) {
+        if (k < warp) before += t.scan[k];
+        U += t.scan[k];
+    }
+    const Share s = share_units<kRuns>(U, gridDim.x, min_run);
+    if (mine > 0) {
+        // the CTA's runs that start in this thread's rows
+        const int w0 = blockIdx.x * s.per_cta;
+        for (int k = 0; k < s.per_cta && w0 + k < s.W; ++k) {
+            const int64_t at = run_start(s, w0 + k);
+            if (at < before || at >= before + mine) continue;
+            int64_t left = at - before;
+            int r = r0, n = first;
+            while (left >= n) {
+                left -= n;
+                n = count(++r);
+            }
+            t.row[k] = r;
+            t.off[k] = (int)left;
+        }
+    }
+    __syncthreads();
+    return s;
+}
+
+}  // namespace kvc

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -111,16 +112,16 @@ def lib() -> ctypes.CDLL:
             "kvc_append_tokens": (ctypes.c_int, [pc, vp, vp, vp, i32, ctypes.c_uint8, vp, vp, vp, vp, ctypes.c_size_t,
                                                  vp, vp]),
             "kvc_reserve_workspace_bytes": (ctypes.c_size_t, [i32]),
-            "kvc_reserve_slots": (ctypes.c_int, [pc, vp, vp, ctypes.c_uint8, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+            "kvc_reserve_slots": (ctypes.c_int, [vp, vp, vp, ctypes.c_uint8, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
                                                  ctypes.c_size_t, vp, vp]),
-            "kvc_norm_rope_write": (ctypes.c_int, [pc, vp, i64, i32, vp, i32, vp, vp, f32, vp, i32, u32, vp, vp, vp, vp,
+            "kvc_norm_rope_write": (ctypes.c_int, [vp, vp, i64, i32, vp, i32, vp, vp, f32, vp, i32, u32, vp, vp, vp, vp,
                                                    vp]),
-            "kvc_block_bounds": (ctypes.c_int, [pc, vp, vp, vp, vp, vp]),
+            "kvc_block_bounds": (ctypes.c_int, [vp, vp, vp, vp, vp, vp]),
             "kvc_select_blocks_workspace_bytes": (ctypes.c_size_t, [i32, i32]),
-            "kvc_select_blocks": (ctypes.c_int, [pc, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp,
+            "kvc_select_blocks": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, ctypes.c_size_t, vp,
                                                  vp]),
             "kvc_block_attention_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
-            "kvc_block_attention": (ctypes.c_int, [pc, vp, vp, i32, vp, i32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]),
+            "kvc_block_attention": (ctypes.c_int, [vp, vp, vp, i32, vp, i32, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -372,30 +373,68 @@ def kvc_step_scores(cache: Cache, scores: torch.Tensor, step_start: torch.Tensor
            "kvc_step_scores")
 
 
-def _call(name: str, cache: Cache, args, tensors, stream):
-    """Call entry point `name` on the cache's device: `tensors` (name, tensor or None) must live there, and the call
-    goes to `stream` or that device's current stream."""
-    dev = cache.k_pool.device
-    for what, t in tensors:
-        if t is not None and t.device != dev:
-            raise KvcError(f"{what}: on {t.device}, the cache is on {dev}")
-    if dev.type != "cuda":
-        raise KvcError(f"{name}: the cache is on {dev}, expected a CUDA device")
-    if dev.index != torch.cuda.current_device():
+# kvc_cache as bytes: the calls below are made once per layer and token, and packing is a third of the cost of a Structure
+_CACHE = struct.Struct("@PPqiiiiPPPPiiii")
+assert _CACHE.size == ctypes.sizeof(KvcCache)
+_DTYPE = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _arg(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
+    """Address of t, a contiguous tensor of exactly this shape and dtype on CUDA device `dev` (-1: not a CUDA device)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _expect(t, name, shape, dtype)
+    raise KvcError(f"{name}: on {t.device}, the cache is on {'cuda:%d' % dev if dev >= 0 else 'no CUDA device'}")
+
+
+def _opt(t: Optional[torch.Tensor], name: str, shape, dtype, dev: int):
+    return None if t is None else _arg(t, name, shape, dtype, dev)
+
+
+def _work(t: torch.Tensor, dev: int):
+    """Address and bytes of a workspace (any dtype) and a check that it lies on the cache's device."""
+    if not t.is_contiguous():
+        raise KvcError("workspace must be contiguous")
+    if t.get_device() != dev:
+        raise KvcError(f"workspace: on {t.device}, the cache is elsewhere")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _cache_args(cache: Cache):
+    """(kvc_cache as bytes, rows, max_pages, page_size, head_dim, dtype, device) of a cache; its tables must lie with its
+    pools and have its shapes."""
+    k, v, bt = cache.k_pool, cache.v_pool, cache.block_table
+    pages, P, D = k.shape
+    S, L, H = cache.num_seqs, cache.num_layers, cache.num_kv_heads
+    dt, dev, rows, mp = k.dtype, k.get_device(), S * L * H, bt.shape[1]
+    if dt not in _DTYPE:
+        raise KvcError(f"k_pool: dtype {dt}, expected torch.float32 or torch.bfloat16")
+    packed = _CACHE.pack(_arg(k, "k_pool", (pages, P, D), dt, dev), _arg(v, "v_pool", (pages, P, D), dt, dev), pages, P, D,
+                         _DTYPE[dt], mp, bt.data_ptr(), cache.row_len.data_ptr(), cache.slot_pos.data_ptr(),
+                         0 if cache.slot_label is None else cache.slot_label.data_ptr(), S, L, H, 0)
+    return packed, rows, mp, P, D, dt, dev
+
+
+def _tables(cache: Cache, rows: int, mp: int, P: int, dev: int):
+    """Check the tables of a cache whose rows are read or written."""
+    _arg(cache.block_table, "block_table", (rows, mp), _I32, dev)
+    _arg(cache.row_len, "row_len", (rows,), _I32, dev)
+    _arg(cache.slot_pos, "slot_pos", (rows, mp * P), _I32, dev)
+
+
+def _call(name: str, dev: int, stream, *args):
+    """Call entry point `name` with the cache's device current, on `stream` or that device's current stream."""
+    if dev < 0:
+        raise KvcError(f"{name}: the cache is not on a CUDA device")
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(name, cache, args, (), stream)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
-    st = st.cuda_stream if hasattr(st, "cuda_stream") else int(st)
-    cs = cache.struct()
-    _check(getattr(lib(), name)(ctypes.byref(cs), *args, st), name)
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _nbytes(t: torch.Tensor) -> int:
-    return t.numel() * t.element_size()
+            return _call(name, dev, stream, *args)
+    st = _raw_stream(dev) if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    status = getattr(_lib or lib(), name)(*args, st)
+    if status != KVC_OK:
+        _check(status, name)
 
 
 def kvc_reserve_workspace_bytes(rows: int) -> int:
@@ -409,28 +448,22 @@ def kvc_reserve_slots(cache: Cache, new_count: torch.Tensor, next_pos: torch.Ten
                       stream=None):
     """Slots for new_count[s] new tokens of each sequence.  token_start: [S + 1] int32; token_pos: [max_tokens] int32;
     slot_map: [max_tokens][L][Hkv] int64; row_len_out and free_count_out may be cache.row_len and free_count."""
-    S, T, i32 = cache.num_seqs, token_pos.numel(), torch.int32
-    _expect(new_count, "new_count", (S,), i32)
-    _expect(next_pos, "next_pos", (S,), i32)
-    if crf is not None:
-        _expect(crf, "crf", (cache.rows, cache.max_slots), torch.float32)
-    _expect(free_pages, "free_pages", (None,), i32)
-    _expect(free_count, "free_count", (1,), torch.int64)
-    _expect(row_len_out, "row_len_out", (cache.rows,), i32)
-    _expect(free_count_out, "free_count_out", (1,), torch.int64)
-    _expect(token_start, "token_start", (S + 1,), i32)
-    _expect(token_pos, "token_pos", (T,), i32)
-    _expect(slot_map, "slot_map", (T, cache.num_layers, cache.num_kv_heads), torch.int64)
+    c, rows, mp, P, _, _, dev = _cache_args(cache)
+    _tables(cache, rows, mp, P, dev)
+    S, T = cache.num_seqs, token_pos.shape[0]
+    if cache.slot_label is not None:
+        _arg(cache.slot_label, "slot_label", (rows, mp * P), torch.uint8, dev)
     if not 0 <= label <= 255:
         raise KvcError(f"label: {label}, expected 0 to 255")
-    _call("kvc_reserve_slots", cache,
-          (_addr(new_count), _addr(next_pos), label, _addr(crf), _addr(free_pages), _addr(free_count), T,
-           _addr(row_len_out), _addr(free_count_out), _addr(token_start), _addr(token_pos), _addr(slot_map),
-           _addr(workspace), _nbytes(workspace), _addr(d_status)),
-          (("new_count", new_count), ("next_pos", next_pos), ("crf", crf), ("free_pages", free_pages),
-           ("free_count", free_count), ("row_len_out", row_len_out), ("free_count_out", free_count_out),
-           ("token_start", token_start), ("token_pos", token_pos), ("slot_map", slot_map), ("workspace", workspace),
-           ("d_status", d_status)), stream)
+    ws, nbytes = _work(workspace, dev)
+    _call("kvc_reserve_slots", dev, stream, c, _arg(new_count, "new_count", (S,), _I32, dev),
+          _arg(next_pos, "next_pos", (S,), _I32, dev), label, _opt(crf, "crf", (rows, mp * P), _F32, dev),
+          _arg(free_pages, "free_pages", (free_pages.shape[0],), _I32, dev),
+          _arg(free_count, "free_count", (1,), _I64, dev), T, _arg(row_len_out, "row_len_out", (rows,), _I32, dev),
+          _arg(free_count_out, "free_count_out", (1,), _I64, dev), _arg(token_start, "token_start", (S + 1,), _I32, dev),
+          _arg(token_pos, "token_pos", (T,), _I32, dev),
+          _arg(slot_map, "slot_map", (T, cache.num_layers, cache.num_kv_heads), _I64, dev), ws, nbytes,
+          _opt(d_status, "d_status", (2,), _I32, dev))
 
 
 def kvc_norm_rope_write(cache: Cache, qkv: torch.Tensor, token_pos: torch.Tensor, slot_map: torch.Tensor,
@@ -441,48 +474,40 @@ def kvc_norm_rope_write(cache: Cache, qkv: torch.Tensor, token_pos: torch.Tensor
     """Norm and rotate the query and key heads of qkv [T][L][Hq + 2 Hkv][D] (tokens may be further apart than their
     size: a slice of a wider array), queries to q_out [T][L][Hq][D], keys and values to the cache slots of slot_map
     [T][L][Hkv].  inv_freq: [rope_dim / 2] fp32 or None for no rotation; token_count: one int32, the tokens present."""
-    L, Hkv, D, dt = cache.num_layers, cache.num_kv_heads, cache.k_pool.shape[2], cache.k_pool.dtype
-    if qkv.dim() != 4 or qkv.shape[1] != L or qkv.shape[3] != D or qkv.shape[2] <= 2 * Hkv:
-        raise KvcError(f"qkv: shape {tuple(qkv.shape)}, expected (*, {L}, Hq + {2 * Hkv}, {D})")
-    T, Hq = qkv.shape[0], qkv.shape[2] - 2 * Hkv
-    if qkv.dtype != dt:
+    c, _, _, _, D, dt, dev = _cache_args(cache)
+    L, H = cache.num_layers, cache.num_kv_heads
+    if qkv.dim() != 4 or qkv.shape[1] != L or qkv.shape[3] != D or qkv.shape[2] <= 2 * H:
+        raise KvcError(f"qkv: shape {tuple(qkv.shape)}, expected (*, {L}, Hq + {2 * H}, {D})")
+    T, heads = qkv.shape[0], qkv.shape[2]
+    Hq, token = heads - 2 * H, L * heads * D
+    if qkv.dtype is not dt:
         raise KvcError(f"qkv: dtype {qkv.dtype}, expected {dt}")
-    stride = L * (Hq + 2 * Hkv) * D
-    if T > 1:
-        stride = max(stride, qkv.stride(0)) if qkv[0].is_contiguous() else -1
-        if stride != qkv.stride(0):
+    if qkv.get_device() != dev:
+        raise KvcError(f"qkv: on {qkv.device}, the cache is elsewhere")
+    apart = token
+    if not qkv.is_contiguous():
+        apart = qkv.stride(0)
+        if not qkv[0].is_contiguous() or (T > 1 and apart < token):
             raise KvcError("qkv must be contiguous within a token, and tokens may not overlap")
-    elif not qkv.is_contiguous():
-        raise KvcError("qkv must be contiguous within a token")
-    _expect(q_out, "q_out", (T, L, Hq, D), dt)
-    _expect(token_pos, "token_pos", (T,), torch.int32)
-    _expect(slot_map, "slot_map", (T, L, Hkv), torch.int64)
-    for what, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _expect(w, what, (L, D), dt)
-    if inv_freq is not None:
-        _expect(inv_freq, "inv_freq", (None,), torch.float32)
-    if token_count is not None:
-        _expect(token_count, "token_count", (1,), torch.int32)
-    _call("kvc_norm_rope_write", cache,
-          (_addr(qkv), stride, T, _addr(token_count), Hq, _addr(q_weight), _addr(k_weight), eps, _addr(inv_freq),
-           0 if inv_freq is None else 2 * inv_freq.numel(), KVC_ROPE_INTERLEAVED if interleaved else 0,
-           _addr(token_pos), _addr(slot_map), _addr(q_out), _addr(d_status)),
-          (("qkv", qkv), ("token_pos", token_pos), ("slot_map", slot_map), ("q_out", q_out), ("q_weight", q_weight),
-           ("k_weight", k_weight), ("inv_freq", inv_freq), ("token_count", token_count), ("d_status", d_status)), stream)
+        apart = max(apart, token)
+    half = 0 if inv_freq is None else inv_freq.shape[0]
+    _call("kvc_norm_rope_write", dev, stream, c, qkv.data_ptr(), apart, T,
+          _opt(token_count, "token_count", (1,), _I32, dev), Hq, _opt(q_weight, "q_weight", (L, D), dt, dev),
+          _opt(k_weight, "k_weight", (L, D), dt, dev), eps, _opt(inv_freq, "inv_freq", (half,), _F32, dev), 2 * half,
+          KVC_ROPE_INTERLEAVED if interleaved else 0, _arg(token_pos, "token_pos", (T,), _I32, dev),
+          _arg(slot_map, "slot_map", (T, L, H), _I64, dev), _arg(q_out, "q_out", (T, L, Hq, D), dt, dev),
+          _opt(d_status, "d_status", (2,), _I32, dev))
 
 
 def kvc_block_bounds(cache: Cache, bounds: torch.Tensor, block_pos: torch.Tensor,
                      from_len: Optional[torch.Tensor] = None, d_status=None, stream=None):
     """Minimum and maximum of every page's keys: bounds [rows][max_pages][2][D] in the cache dtype, block_pos
     [rows][max_pages] int32 (lowest position); from_len [rows] int32: only the pages from that slot on."""
-    rows, mp = cache.block_table.shape
-    _expect(bounds, "bounds", (rows, mp, 2, cache.k_pool.shape[2]), cache.k_pool.dtype)
-    _expect(block_pos, "block_pos", (rows, mp), torch.int32)
-    if from_len is not None:
-        _expect(from_len, "from_len", (rows,), torch.int32)
-    _call("kvc_block_bounds", cache, (_addr(from_len), _addr(bounds), _addr(block_pos), _addr(d_status)),
-          (("bounds", bounds), ("block_pos", block_pos), ("from_len", from_len), ("d_status", d_status)), stream)
+    c, rows, mp, P, D, dt, dev = _cache_args(cache)
+    _tables(cache, rows, mp, P, dev)
+    _call("kvc_block_bounds", dev, stream, c, _opt(from_len, "from_len", (rows,), _I32, dev),
+          _arg(bounds, "bounds", (rows, mp, 2, D), dt, dev), _arg(block_pos, "block_pos", (rows, mp), _I32, dev),
+          _opt(d_status, "d_status", (2,), _I32, dev))
 
 
 def kvc_select_blocks_workspace_bytes(rows: int, max_pages_per_row: int) -> int:
@@ -495,19 +520,15 @@ def kvc_select_blocks(cache: Cache, bounds: torch.Tensor, block_pos: torch.Tenso
     """The top_k = block_list.shape[1] pages of each row with the highest bound on the group's logits, the first
     sink_blocks and last recent_blocks always among them: block_list [rows][top_k] int32 ascending, then -1;
     block_count [rows] int32."""
-    rows, mp = cache.block_table.shape
-    D, dt = cache.k_pool.shape[2], cache.k_pool.dtype
-    _expect(bounds, "bounds", (rows, mp, 2, D), dt)
-    _expect(block_pos, "block_pos", (rows, mp), torch.int32)
-    _expect(q, "q", (cache.num_seqs, cache.num_layers, None, D), dt)
-    _expect(q_pos, "q_pos", (cache.num_seqs,), torch.int32)
-    _expect(block_list, "block_list", (rows, None), torch.int32)
-    _expect(block_count, "block_count", (rows,), torch.int32)
-    _call("kvc_select_blocks", cache,
-          (_addr(bounds), _addr(block_pos), _addr(q), _addr(q_pos), q.shape[2], block_list.shape[1], sink_blocks,
-           recent_blocks, _addr(block_list), _addr(block_count), _addr(workspace), _nbytes(workspace), _addr(d_status)),
-          (("bounds", bounds), ("block_pos", block_pos), ("q", q), ("q_pos", q_pos), ("block_list", block_list),
-           ("block_count", block_count), ("workspace", workspace), ("d_status", d_status)), stream)
+    c, rows, mp, P, D, dt, dev = _cache_args(cache)
+    _tables(cache, rows, mp, P, dev)
+    S, L, Hq, k = cache.num_seqs, cache.num_layers, q.shape[2], block_list.shape[1]
+    ws, nbytes = _work(workspace, dev)
+    _call("kvc_select_blocks", dev, stream, c, _arg(bounds, "bounds", (rows, mp, 2, D), dt, dev),
+          _arg(block_pos, "block_pos", (rows, mp), _I32, dev), _arg(q, "q", (S, L, Hq, D), dt, dev),
+          _arg(q_pos, "q_pos", (S,), _I32, dev), Hq, k, sink_blocks, recent_blocks,
+          _arg(block_list, "block_list", (rows, k), _I32, dev), _arg(block_count, "block_count", (rows,), _I32, dev), ws,
+          nbytes, _opt(d_status, "d_status", (2,), _I32, dev))
 
 
 def kvc_block_attention_workspace_bytes(rows: int, group: int, head_dim: int) -> int:
@@ -520,22 +541,17 @@ def kvc_block_attention(cache: Cache, q: torch.Tensor, q_pos: torch.Tensor, out:
     """Attention of one new token over the listed pages (block_list [rows][stride] int32 ascending, block_count [rows]
     int32), or over the whole rows without a list.  q: [S][L][Hq][D] in the cache dtype; q_pos: [S] int32; out:
     [S][L][Hq][D] fp32; lse: [S][L][Hq] fp32."""
-    S, L, D = cache.num_seqs, cache.num_layers, cache.k_pool.shape[2]
-    _expect(q, "q", (S, L, None, D), cache.k_pool.dtype)
-    Hq = q.shape[2]
-    _expect(q_pos, "q_pos", (S,), torch.int32)
-    _expect(out, "out", (S, L, Hq, D), torch.float32)
-    _expect(lse, "lse", (S, L, Hq), torch.float32)
+    c, rows, mp, P, D, dt, dev = _cache_args(cache)
+    _tables(cache, rows, mp, P, dev)
     if (block_list is None) != (block_count is None):
         raise KvcError("block_list and block_count go together")
-    if block_list is not None:
-        _expect(block_list, "block_list", (cache.rows, None), torch.int32)
-        _expect(block_count, "block_count", (cache.rows,), torch.int32)
-    _call("kvc_block_attention", cache,
-          (_addr(q), _addr(q_pos), Hq, _addr(block_list), 0 if block_list is None else block_list.shape[1],
-           _addr(block_count), _addr(out), _addr(lse), _addr(workspace), _nbytes(workspace), _addr(d_status)),
-          (("q", q), ("q_pos", q_pos), ("out", out), ("lse", lse), ("workspace", workspace), ("block_list", block_list),
-           ("block_count", block_count), ("d_status", d_status)), stream)
+    S, L, Hq = cache.num_seqs, cache.num_layers, q.shape[2]
+    apart = 0 if block_list is None else block_list.shape[1]
+    ws, nbytes = _work(workspace, dev)
+    _call("kvc_block_attention", dev, stream, c, _arg(q, "q", (S, L, Hq, D), dt, dev), _arg(q_pos, "q_pos", (S,), _I32, dev),
+          Hq, _opt(block_list, "block_list", (rows, apart), _I32, dev), apart,
+          _opt(block_count, "block_count", (rows,), _I32, dev), _arg(out, "out", (S, L, Hq, D), _F32, dev),
+          _arg(lse, "lse", (S, L, Hq), _F32, dev), ws, nbytes, _opt(d_status, "d_status", (2,), _I32, dev))
 
 
 def ratchet_seq_states(state: torch.Tensor, num_seqs: int):
