@@ -111,16 +111,17 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&w)[3]) {
 // slots of row r that take part, in list order (0 for a row whose length or list is not usable; `tell` reports it)
 __device__ __forceinline__ int row_slots(const AttnArgs &a, int r, bool tell) {
     const CacheView &c = a.c;
-    const int n = c.row_len[r], P = c.page_size;
+    const int n = c.row_len[r], k = a.list ? a.list_len[r] : 0, P = c.page_size;  // one round trip for both
+    const bool in = !a.list || (k > 0 && k <= a.list_stride);
+    const int last = a.list && in ? a.list[(int64_t)r * a.list_stride + k - 1] : 0;
     if (n < 0 || n > c.max_slots) {
         if (tell) report(a.status, KVC_DEV_BAD_LENGTH, r);
         return 0;
     }
     if (!a.list) return n;
-    const int k = a.list_len[r], nb = (n + P - 1) / P;
+    const int nb = (n + P - 1) / P;
     if (k == 0) return 0;
-    const int last = k > 0 && k <= a.list_stride ? a.list[(int64_t)r * a.list_stride + k - 1] : -1;
-    if (k > nb || last < 0 || last >= nb) {
+    if (!in || k > nb || last < 0 || last >= nb) {
         if (tell) report(a.status, KVC_DEV_BAD_LIST, r);
         return 0;
     }
@@ -174,112 +175,167 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     float *head_part = reinterpret_cast<float *>(smem + (size_t)kWarps * kRing * kStage) + warp * rec;
     const int w = blockIdx.x * sh.per_cta + warp;
     const bool works = warp < sh.per_cta && w < sh.W;
-    int64_t left = works ? run_start(sh, w + 1) - run_start(sh, w) : 0;
-    int off = works ? runs.off[warp] : 0;
-    for (int row = works ? runs.row[warp] : 0; left > 0; ++row, off = 0) {
-        const int slots = row_slots(a, row, false);
-        const int nch = (slots + CH - 1) / CH;
-        const int cnt = (int)min((int64_t)(nch - off), left);
-        if (cnt <= 0) continue;
-        left -= cnt;
-        const int n = c.row_len[row], nb = (n + P - 1) / P;
-        const int seq = row / (c.num_layers * Hkv), qpos = a.q_pos[seq];
-        const int64_t hbase = (int64_t)(row / Hkv) * a.num_q_heads + (row % Hkv) * G;
-        const int32_t *bt = c.block_table + (int64_t)row * c.max_pages_per_row;
-        const int32_t *list = a.list ? a.list + (int64_t)row * a.list_stride : nullptr;
-        const int32_t *posr = c.slot_pos + (int64_t)row * c.max_slots;
-        bool bad_page = false, bad_list = false;
+    int total = works ? (int)(run_start(sh, w + 1) - run_start(sh, w)) : 0;  // chunks of the run
 
-        // Page lookups.  kWhole (the page size is a multiple of CH): a chunk lies in one page, and lane l looks up
-        // chunk 32 j + l of the run, a batch of 32 chunks ahead of its use.  Else every lane looks up the page of its own
-        // key, one chunk ahead.  `slot` is the key's (chunk's first) logical slot, -1 where there is none to read.
-        auto look = [&](int stream, int &slot, int64_t &src) {
-            slot = -1;
-            src = 0;
-            if (stream < 0 || stream >= slots) return;
-            const int j = stream / P, o = stream - j * P;
-            int b = j;
-            if (list) {
-                b = list[j];
-                if (b < 0 || b >= nb || (j > 0 && list[j - 1] >= b)) {
-                    bad_list = true;
-                    return;
-                }
-            }
-            const int32_t pg = bt[b];
-            if (pg < 0 || pg >= c.num_pages) {
-                bad_page = true;
+    // Lookups.  Lane l of batch j knows chunk 32 j + l of the run: its row, its place in the row's chunks and how many follow
+    // it there, and, where a chunk lies in one page (kWhole: the page size is a multiple of CH), its first slot (-1: not
+    // readable), where that is in the pool, and its keys.  A batch is filled a batch ahead of its use, so that the run's
+    // loads go on across rows.  Else every lane looks up the page of its own key, one chunk ahead.
+    int b_row[2], b_off[2], b_left[2], b_slot[2], b_keys[2];
+    int64_t b_src[2];
+    int crow = works ? runs.row[warp] : 0, coff = works ? runs.off[warp] : 0;  // the next chunk to look up
+    int cslots = total > 0 ? row_slots(a, crow, false) : 0;
+    auto look = [&](int row, int stream, int slots, int &slot, int64_t &src, int &keys) {
+        slot = -1;
+        src = 0;
+        keys = 0;
+        if (stream >= slots) return;
+        const int j = stream / P, o = stream - j * P, n = c.row_len[row];
+        int b = j;
+        if (a.list) {
+            const int32_t *list = a.list + (int64_t)row * a.list_stride;
+            b = list[j];
+            if (b < 0 || (int64_t)b * P >= n || (j > 0 && list[j - 1] >= b)) {
+                report(a.status, KVC_DEV_BAD_LIST, row);
                 return;
             }
-            slot = b * P + o;
-            src = (int64_t)pg * P + o;
-        };
-        int sl[2] = {-1, -1};
-        int64_t sr[2] = {0, 0};
-        if constexpr (kWhole) {
-            look(lane < cnt ? (off + lane) * CH : -1, sl[0], sr[0]);
-            look(32 + lane < cnt ? (off + 32 + lane) * CH : -1, sl[1], sr[1]);
-        } else {
-            look((off)*CH + (lane & (CH - 1)), sl[0], sr[0]);
         }
-        uint32_t ok[kRing];  // the stages' readable keys, a bit each
+        const int32_t pg = c.block_table[(int64_t)row * c.max_pages_per_row + b];
+        if (pg < 0 || pg >= c.num_pages) {
+            report(a.status, KVC_DEV_BAD_PAGE, row);
+            return;
+        }
+        slot = b * P + o;
+        src = (int64_t)pg * P + o;
+        keys = min(CH, n - slot);  // the page may end behind the row's last slot
+    };
+    auto fill = [&](int base, int &brow, int &boff, int &bleft, int &bslot, int64_t &bsrc, int &bkeys) {
+        const int need = min(32, total - base);
+        if (need <= 0) return;
+        int row = crow, o = coff + lane, slots = cslots;
+        if ((cslots + CH - 1) / CH - coff > need) {
+            coff += need;
+        } else {  // the batch goes on in the rows after crow, 32 of them at a time
+            int got = 0;
+            for (int r = crow, o0 = coff;; r += 32, o0 = 0) {
+                if (r >= c.rows) {  // only if the lengths changed meanwhile
+                    total = base + got;
+                    break;
+                }
+                const int sl = r + lane < c.rows ? row_slots(a, r + lane, false) : 0;
+                const int have = (sl + CH - 1) / CH - (lane == 0 ? o0 : 0);
+                int incl = have;
 #pragma unroll
-        for (int i = 0; i < kRing; ++i) ok[i] = 0;
-        // stage `st` takes chunk i of the run; returns its readable keys
-        auto issue = [&](int i, int st) -> uint32_t {
-            uint32_t m = 0;
-            if (i < cnt) {
-                const uint32_t dst = smem_u32(ring + (size_t)st * kStage);
-                if constexpr (kWhole) {
-                    const int which = (i >> 5) & 1;
-                    const int s0 = __shfl_sync(0xffffffffu, which ? sl[1] : sl[0], i & 31);
-                    const int64_t src = __shfl_sync(0xffffffffu, which ? sr[1] : sr[0], i & 31);
-                    if (s0 >= 0) {
-                        const char *ks = reinterpret_cast<const char *>(kp + src * D);
-                        const char *vs = reinterpret_cast<const char *>(vp + src * D);
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, x);
+                    if (lane >= x) incl += y;
+                }
+                const int all = __shfl_sync(0xffffffffu, incl, 31), x = lane - got;
+                int k = 0;  // the row of this lane's chunk: the number of rows that end at or before it
 #pragma unroll
-                        for (uint32_t e = 0; e < (uint32_t)(CH * PC / 32); ++e) {
-                            // piece p of key r lands at piece p ^ (r & 7): the eight rows of an ldmatrix phase then
-                            // fall in distinct banks
-                            const uint32_t x = e * 32 + lane, r = x / PC, p = x % PC;
-                            const uint32_t db = r * RB + ((MM ? (p ^ (r & 7)) : p) << 4);
-                            cp16(dst + db, ks + x * 16);
-                            cp16(dst + kHalf + db, vs + x * 16);
-                        }
-                        if (lane < CH) cp4(dst + 2 * kHalf + lane * 4, posr + s0 + lane);
-                        const int here = min(CH, n - s0);
-                        m = here >= CH ? (1u << CH) - 1 : (1u << max(here, 0)) - 1;
-                    }
-                } else {
-                    const bool mine = sl[0] >= 0 && sl[0] < n;
-                    m = __ballot_sync(0xffffffffu, mine) & ((1u << CH) - 1);
+                for (int half = 16; half > 0; half >>= 1)
+                    if (x >= __shfl_sync(0xffffffffu, incl, k + half - 1)) k += half;
+                const int before = __shfl_sync(0xffffffffu, incl - have, k), s = __shfl_sync(0xffffffffu, sl, k);
+                if (x >= 0 && x < all) {
+                    row = r + k;
+                    o = x - before + (k == 0 ? o0 : 0);
+                    slots = s;
+                }
+                got += all;
+                if (got >= need) break;
+            }
+            crow = __shfl_sync(0xffffffffu, row, need - 1);
+            coff = __shfl_sync(0xffffffffu, o, need - 1) + 1;
+            cslots = __shfl_sync(0xffffffffu, slots, need - 1);
+        }
+        brow = row;
+        boff = o;
+        bleft = (slots + CH - 1) / CH - 1 - o;
+        if constexpr (kWhole) {
+            if (lane < need) look(row, o * CH, slots, bslot, bsrc, bkeys);
+        } else {
+            bslot = slots;
+        }
+    };
+    // x[which] of lane l
+    auto pick = [&](const auto (&x)[2], int i) { return __shfl_sync(0xffffffffu, ((i >> 5) & 1) ? x[1] : x[0], i & 31); };
+    fill(0, b_row[0], b_off[0], b_left[0], b_slot[0], b_src[0], b_keys[0]);
+    fill(32, b_row[1], b_off[1], b_left[1], b_slot[1], b_src[1], b_keys[1]);
+    int k_row = 0, k_slot = -1, k_keys = 0;  // this lane's key of the next chunk to load (pages that are no multiple of CH)
+    int64_t k_src = 0;
+    auto look_key = [&](int i) {
+        if (i >= total) return;
+        k_row = pick(b_row, i);
+        const int o = pick(b_off, i), slots = pick(b_slot, i);
+        look(k_row, o * CH + (lane & (CH - 1)), slots, k_slot, k_src, k_keys);
+    };
+    if constexpr (!kWhole) look_key(0);
+    uint32_t ok[kRing];  // the stages' readable keys, a bit each
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) ok[i] = 0;
+    // stage `st` takes chunk i of the run; returns its readable keys
+    auto issue = [&](int i, int st) -> uint32_t {
+        uint32_t m = 0;
+        if (i < total) {
+            const uint32_t dst = smem_u32(ring + (size_t)st * kStage);
+            if constexpr (kWhole) {
+                const int s0 = pick(b_slot, i), row = pick(b_row, i), keys = pick(b_keys, i);
+                const int64_t src = pick(b_src, i);
+                if (s0 >= 0) {
+                    const char *ks = reinterpret_cast<const char *>(kp + src * D);
+                    const char *vs = reinterpret_cast<const char *>(vp + src * D);
 #pragma unroll
                     for (uint32_t e = 0; e < (uint32_t)(CH * PC / 32); ++e) {
+                        // piece p of key r lands at piece p ^ (r & 7): the eight rows of an ldmatrix phase then fall in
+                        // distinct banks
                         const uint32_t x = e * 32 + lane, r = x / PC, p = x % PC;
-                        const int64_t src = __shfl_sync(0xffffffffu, sr[0], r);
                         const uint32_t db = r * RB + ((MM ? (p ^ (r & 7)) : p) << 4);
-                        if ((m >> r) & 1u) {
-                            cp16(dst + db, reinterpret_cast<const char *>(kp + src * D) + p * 16);
-                            cp16(dst + kHalf + db, reinterpret_cast<const char *>(vp + src * D) + p * 16);
-                        }
+                        cp16(dst + db, ks + x * 16);
+                        cp16(dst + kHalf + db, vs + x * 16);
                     }
-                    if (lane < CH && mine) cp4(dst + 2 * kHalf + lane * 4, posr + sl[0]);
-                    look(i + 1 < cnt ? (off + i + 1) * CH + (lane & (CH - 1)) : -1, sl[0], sr[0]);
+                    if (lane < CH) cp4(dst + 2 * kHalf + lane * 4, c.slot_pos + (int64_t)row * c.max_slots + s0 + lane);
+                    m = (1u << keys) - 1;
                 }
-            }
-            cp_commit();  // one group a call, empty or not, so that the group count stays in step
-            return m;
-        };
+            } else {
+                const bool mine = k_keys > 0;
+                m = __ballot_sync(0xffffffffu, mine) & ((1u << CH) - 1);
 #pragma unroll
-        for (int i = 0; i < kRing - 1; ++i) ok[i] = issue(i, i);
+                for (uint32_t e = 0; e < (uint32_t)(CH * PC / 32); ++e) {
+                    const uint32_t x = e * 32 + lane, r = x / PC, p = x % PC;
+                    const int64_t src = __shfl_sync(0xffffffffu, k_src, r);
+                    const uint32_t db = r * RB + ((MM ? (p ^ (r & 7)) : p) << 4);
+                    if ((m >> r) & 1u) {
+                        cp16(dst + db, reinterpret_cast<const char *>(kp + src * D) + p * 16);
+                        cp16(dst + kHalf + db, reinterpret_cast<const char *>(vp + src * D) + p * 16);
+                    }
+                }
+                if (lane < CH && mine) cp4(dst + 2 * kHalf + lane * 4, c.slot_pos + (int64_t)k_row * c.max_slots + k_slot);
+                look_key(i + 1);
+            }
+        }
+        cp_commit();  // one group a call, empty or not, so that the group count stays in step
+        return m;
+    };
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) ok[i] = issue(i, i);
 
-        // bf16: a lane holds heads hm = 2 (lane % 4) and hm + 1; O[d][h] for d = 16 t + lane / 4 (+ 8).  fp32: a lane holds
-        // elements d0 .. d0 + 3 and D / 2 + d0 .. + 3 of every head
-        float mm[2] = {-INFINITY, -INFINITY}, ms[2] = {0.f, 0.f};
-        float oc[MM ? NS : 1][4];
-        uint32_t qb[MM ? NS : 1][2];
-        float m[MM ? 1 : GM], s[MM ? 1 : GM], o[MM ? 1 : GM][8], qv[MM ? 1 : GM][8];
-        const int kslot = lane / LK, d0 = (lane % LK) * 4;
+    // bf16: a lane holds heads hm = 2 (lane % 4) and hm + 1; O[d][h] for d = 16 t + lane / 4 (+ 8).  fp32: a lane holds
+    // elements d0 .. d0 + 3 and D / 2 + d0 .. + 3 of every head
+    float mm[2], ms[2];
+    float oc[MM ? NS : 1][4];
+    uint32_t qb[MM ? NS : 1][2];
+    float m[MM ? 1 : GM], s[MM ? 1 : GM], o[MM ? 1 : GM][8], qv[MM ? 1 : GM][8];
+    const int kslot = lane / LK, d0 = (lane % LK) * 4;
+    int row = -1, qpos = 0;  // the row of the chunk at hand, -1 between rows
+    int64_t hbase = 0;
+    bool begins = false;
+    auto begin_row = [&](int i) {
+        row = pick(b_row, i);
+        begins = pick(b_off, i) == 0;
+        qpos = a.q_pos[row / (c.num_layers * Hkv)];
+        hbase = (int64_t)(row / Hkv) * a.num_q_heads + (row % Hkv) * G;
+        mm[0] = mm[1] = -INFINITY;
+        ms[0] = ms[1] = 0.f;
         if constexpr (MM) {
             const int hq = lane >> 2;
             const uint16_t *qg = reinterpret_cast<const uint16_t *>(static_cast<const T *>(a.q) + (hbase + hq) * D);
@@ -306,168 +362,166 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
                 }
             }
         }
+    };
 
-        int st = 0;
-        for (int i = 0; i < cnt; ++i) {
-            {
-                const int k = i + kRing - 1, sk = st == 0 ? kRing - 1 : st - 1;
-                if constexpr (kWhole) {
-                    if ((k & 31) == 0 && k >= 32) {  // batch k / 32 begins; the one before it makes room for the next
-                        const int x = k + 32 + lane;
-                        if ((k >> 5) & 1) look(x < cnt ? (off + x) * CH : -1, sl[0], sr[0]);
-                        else look(x < cnt ? (off + x) * CH : -1, sl[1], sr[1]);
-                    }
-                }
-                const uint32_t mk = issue(k, sk);
-#pragma unroll
-                for (int x = 0; x < kRing; ++x)
-                    if (x == sk) ok[x] = mk;
+    int st = 0;
+    for (int i = 0; i < total; ++i) {
+        if (row < 0) begin_row(i);
+        {
+            const int k = i + kRing - 1, sk = st == 0 ? kRing - 1 : st - 1;
+            if ((k & 31) == 4 && k > 32) {  // batch k / 32 - 1 is consumed: batch k / 32 + 1 takes its place
+                const int base = (k & ~31) + 32;
+                if ((k >> 5) & 1) fill(base, b_row[0], b_off[0], b_left[0], b_slot[0], b_src[0], b_keys[0]);
+                else fill(base, b_row[1], b_off[1], b_left[1], b_slot[1], b_src[1], b_keys[1]);
             }
-            cp_wait<kRing - 1>();  // this lane's copies of chunk i have landed
-            __syncwarp();          // and so have the other lanes'
-            uint32_t vis = 0;
+            const uint32_t mk = issue(k, sk);
 #pragma unroll
             for (int x = 0; x < kRing; ++x)
-                if (x == st) vis = ok[x];
-            unsigned char *stage = ring + (size_t)st * kStage;
-            const int32_t *ps = reinterpret_cast<const int32_t *>(stage + 2 * kHalf);
-            vis &= __ballot_sync(0xffffffffu, lane < CH && ps[lane & (CH - 1)] <= qpos);
-            if constexpr (MM) {
-                const uint32_t kb = smem_u32(stage), vb = kb + kHalf;
-                if (vis != (1u << CH) - 1) {  // hidden keys' V rows are zeroed: their P is 0, and 0 * NaN is not
-                    for (int e = lane; e < CH * PC; e += 32)
-                        if (!((vis >> (e / PC)) & 1u))
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + e * 16), "r"(0u) : "memory");
-                    __syncwarp();
+                if (x == sk) ok[x] = mk;
+        }
+        cp_wait<kRing - 1>();  // this lane's copies of chunk i have landed
+        __syncwarp();          // and so have the other lanes'
+        uint32_t vis = 0;
+#pragma unroll
+        for (int x = 0; x < kRing; ++x)
+            if (x == st) vis = ok[x];
+        unsigned char *stage = ring + (size_t)st * kStage;
+        const int32_t *ps = reinterpret_cast<const int32_t *>(stage + 2 * kHalf);
+        vis &= __ballot_sync(0xffffffffu, lane < CH && ps[lane & (CH - 1)] <= qpos);
+        if constexpr (MM) {
+            const uint32_t kb = smem_u32(stage), vb = kb + kHalf;
+            if (vis != (1u << CH) - 1) {  // hidden keys' V rows are zeroed: their P is 0, and 0 * NaN is not
+                for (int e = lane; e < CH * PC; e += 32)
+                    if (!((vis >> (e / PC)) & 1u))
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + e * 16), "r"(0u) : "memory");
+                __syncwarp();
+            }
+            // S[key][head]: ldmatrix phase x reads keys (lane & 7) + 8 (x & 1), piece 2 t + x / 2
+            float sc[4] = {0.f, 0.f, 0.f, 0.f};
+            {
+                const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
+                const uint32_t rowa = kb + key * RB;
+#pragma unroll
+                for (int t = 0; t < NS; ++t) {
+                    uint32_t af[4];
+                    ldsm_x4(rowa + ((((uint32_t)(2 * t + (lane >> 4))) ^ (key & 7)) << 4), af);
+                    mma16816(sc, af, qb[t][0], qb[t][1]);
                 }
-                // S[key][head]: ldmatrix phase x reads keys (lane & 7) + 8 (x & 1), piece 2 t + x / 2
-                float sc[4] = {0.f, 0.f, 0.f, 0.f};
-                {
-                    const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
-                    const uint32_t rowa = kb + key * RB;
+            }
+            const int ka = lane >> 2;
+            const bool va = (vis >> ka) & 1u, vc = (vis >> (ka + 8)) & 1u;
+            const float l00 = va ? sc[0] * a.scale_log2 : -INFINITY, l01 = va ? sc[1] * a.scale_log2 : -INFINITY;
+            const float l10 = vc ? sc[2] * a.scale_log2 : -INFINITY, l11 = vc ? sc[3] * a.scale_log2 : -INFINITY;
+            float lm0 = fmaxf(l00, l10), lm1 = fmaxf(l01, l11);
+            if (__any_sync(0xffffffffu, lm0 > mm[0] + kSlack || lm1 > mm[1] + kSlack)) {
 #pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-                        uint32_t af[4];
-                        ldsm_x4(rowa + ((((uint32_t)(2 * t + (lane >> 4))) ^ (key & 7)) << 4), af);
-                        mma16816(sc, af, qb[t][0], qb[t][1]);
-                    }
+                for (int x = 4; x < 32; x <<= 1) {
+                    lm0 = fmaxf(lm0, __shfl_xor_sync(0xffffffffu, lm0, x));
+                    lm1 = fmaxf(lm1, __shfl_xor_sync(0xffffffffu, lm1, x));
                 }
-                const int ka = lane >> 2;
-                const bool va = (vis >> ka) & 1u, vc = (vis >> (ka + 8)) & 1u;
-                const float l00 = va ? sc[0] * a.scale_log2 : -INFINITY, l01 = va ? sc[1] * a.scale_log2 : -INFINITY;
-                const float l10 = vc ? sc[2] * a.scale_log2 : -INFINITY, l11 = vc ? sc[3] * a.scale_log2 : -INFINITY;
-                float lm0 = fmaxf(l00, l10), lm1 = fmaxf(l01, l11);
-                if (__any_sync(0xffffffffu, lm0 > mm[0] + kSlack || lm1 > mm[1] + kSlack)) {
+                const float n0 = fmaxf(mm[0], lm0), n1 = fmaxf(mm[1], lm1);
+                const float f0 = weight(mm[0], n0), f1 = weight(mm[1], n1);
+                ms[0] *= f0;
+                ms[1] *= f1;
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) {
-                        lm0 = fmaxf(lm0, __shfl_xor_sync(0xffffffffu, lm0, x));
-                        lm1 = fmaxf(lm1, __shfl_xor_sync(0xffffffffu, lm1, x));
-                    }
-                    const float n0 = fmaxf(mm[0], lm0), n1 = fmaxf(mm[1], lm1);
-                    const float f0 = weight(mm[0], n0), f1 = weight(mm[1], n1);
-                    ms[0] *= f0;
-                    ms[1] *= f1;
-#pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-                        oc[t][0] *= f0;
-                        oc[t][1] *= f1;
-                        oc[t][2] *= f0;
-                        oc[t][3] *= f1;
-                    }
-                    mm[0] = n0;
-                    mm[1] = n1;
+                for (int t = 0; t < NS; ++t) {
+                    oc[t][0] *= f0;
+                    oc[t][1] *= f1;
+                    oc[t][2] *= f0;
+                    oc[t][3] *= f1;
                 }
-                const float p00 = weight(l00, mm[0]), p01 = weight(l01, mm[1]);
-                const float p10 = weight(l10, mm[0]), p11 = weight(l11, mm[1]);
-                ms[0] += p00 + p10;
-                ms[1] += p01 + p11;
-                // P as the B operand [key][head], transposed from the [key][head] rows this lane holds
-                uint32_t pa[3], pb[3];
-                split3(p00, p01, pa);
-                split3(p10, p11, pb);
+                mm[0] = n0;
+                mm[1] = n1;
+            }
+            const float p00 = weight(l00, mm[0]), p01 = weight(l01, mm[1]);
+            const float p10 = weight(l10, mm[0]), p11 = weight(l11, mm[1]);
+            ms[0] += p00 + p10;
+            ms[1] += p01 + p11;
+            // P as the B operand [key][head], transposed from the [key][head] rows this lane holds
+            uint32_t pa[3], pb[3];
+            split3(p00, p01, pa);
+            split3(p10, p11, pb);
 #pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    pa[x] = movm_t(pa[x]);
-                    pb[x] = movm_t(pb[x]);
+            for (int x = 0; x < 3; ++x) {
+                pa[x] = movm_t(pa[x]);
+                pb[x] = movm_t(pb[x]);
+            }
+            // O^T[d][head] += V^T (d x 16 keys) . P: ldmatrix.trans phase x reads keys (lane & 7) + 8 (x / 2), piece
+            // 2 t + (x & 1)
+            {
+                const int key = (lane & 7) + ((lane >> 4) & 1) * 8;
+                const uint32_t rowa = vb + key * RB;
+#pragma unroll
+                for (int t = 0; t < NS; ++t) {
+                    uint32_t af[4];
+                    ldsm_x4_t(rowa + ((((uint32_t)(2 * t + ((lane >> 3) & 1))) ^ (key & 7)) << 4), af);
+                    float pv[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) mma16816(pv, af, pa[x], pb[x]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) oc[t][u] += pv[u];
                 }
-                // O^T[d][head] += V^T (d x 16 keys) . P: ldmatrix.trans phase x reads keys (lane & 7) + 8 (x / 2), piece
-                // 2 t + (x & 1)
-                {
-                    const int key = (lane & 7) + ((lane >> 4) & 1) * 8;
-                    const uint32_t rowa = vb + key * RB;
+            }
+        } else {
+            const float *Ks = reinterpret_cast<const float *>(stage), *Vs = Ks + CH * D;
+            float l[STEPS][GM], cm[GM];
 #pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-                        uint32_t af[4];
-                        ldsm_x4_t(rowa + ((((uint32_t)(2 * t + ((lane >> 3) & 1))) ^ (key & 7)) << 4), af);
-                        float pv[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int g = 0; g < GM; ++g) cm[g] = -INFINITY;
 #pragma unroll
-                        for (int x = 0; x < 3; ++x) mma16816(pv, af, pa[x], pb[x]);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) oc[t][u] += pv[u];
-                    }
-                }
-            } else {
-                const float *Ks = reinterpret_cast<const float *>(stage), *Vs = Ks + CH * D;
-                float l[STEPS][GM], cm[GM];
-#pragma unroll
-                for (int g = 0; g < GM; ++g) cm[g] = -INFINITY;
-#pragma unroll
-                for (int t = 0; t < STEPS; ++t) {
-                    const int key = t * KW + kslot;
-                    const bool v = (vis >> key) & 1u;
-                    const float4 x0 = *reinterpret_cast<const float4 *>(Ks + key * D + d0);
-                    const float4 x1 = *reinterpret_cast<const float4 *>(Ks + key * D + D / 2 + d0);
-#pragma unroll
-                    for (int g = 0; g < GM; ++g) {
-                        float d = qv[g][0] * x0.x + qv[g][1] * x0.y + qv[g][2] * x0.z + qv[g][3] * x0.w;
-                        d += qv[g][4] * x1.x + qv[g][5] * x1.y + qv[g][6] * x1.z + qv[g][7] * x1.w;
-#pragma unroll
-                        for (int x = LK / 2; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-                        l[t][g] = v ? d * a.scale_log2 : -INFINITY;
-                        cm[g] = fmaxf(cm[g], l[t][g]);
-                    }
-                }
+            for (int t = 0; t < STEPS; ++t) {
+                const int key = t * KW + kslot;
+                const bool v = (vis >> key) & 1u;
+                const float4 x0 = *reinterpret_cast<const float4 *>(Ks + key * D + d0);
+                const float4 x1 = *reinterpret_cast<const float4 *>(Ks + key * D + D / 2 + d0);
 #pragma unroll
                 for (int g = 0; g < GM; ++g) {
+                    float d = qv[g][0] * x0.x + qv[g][1] * x0.y + qv[g][2] * x0.z + qv[g][3] * x0.w;
+                    d += qv[g][4] * x1.x + qv[g][5] * x1.y + qv[g][6] * x1.z + qv[g][7] * x1.w;
 #pragma unroll
-                    for (int x = LK; x < 32; x <<= 1) cm[g] = fmaxf(cm[g], __shfl_xor_sync(0xffffffffu, cm[g], x));
-                    if (cm[g] > m[g]) {  // warp-uniform: a new maximum rescales the running sum and output
-                        const float f = weight(m[g], cm[g]);
-                        s[g] *= f;
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) o[g][u] *= f;
-                        m[g] = cm[g];
-                    }
+                    for (int x = LK / 2; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
+                    l[t][g] = v ? d * a.scale_log2 : -INFINITY;
+                    cm[g] = fmaxf(cm[g], l[t][g]);
                 }
+            }
 #pragma unroll
-                for (int t = 0; t < STEPS; ++t) {
-                    const int key = t * KW + kslot;
-                    if ((vis >> key) & 1u) {
-                        const float4 x0 = *reinterpret_cast<const float4 *>(Vs + key * D + d0);
-                        const float4 x1 = *reinterpret_cast<const float4 *>(Vs + key * D + D / 2 + d0);
-                        const float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+            for (int g = 0; g < GM; ++g) {
 #pragma unroll
-                        for (int g = 0; g < GM; ++g) {
-                            const float p = weight(l[t][g], m[g]);
-                            s[g] += p;
+                for (int x = LK; x < 32; x <<= 1) cm[g] = fmaxf(cm[g], __shfl_xor_sync(0xffffffffu, cm[g], x));
+                if (cm[g] > m[g]) {  // warp-uniform: a new maximum rescales the running sum and output
+                    const float f = weight(m[g], cm[g]);
+                    s[g] *= f;
 #pragma unroll
-                            for (int u = 0; u < 8; ++u) o[g][u] = fmaf(p, y[u], o[g][u]);
-                        }
+                    for (int u = 0; u < 8; ++u) o[g][u] *= f;
+                    m[g] = cm[g];
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < STEPS; ++t) {
+                const int key = t * KW + kslot;
+                if ((vis >> key) & 1u) {
+                    const float4 x0 = *reinterpret_cast<const float4 *>(Vs + key * D + d0);
+                    const float4 x1 = *reinterpret_cast<const float4 *>(Vs + key * D + D / 2 + d0);
+                    const float y[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                    for (int g = 0; g < GM; ++g) {
+                        const float p = weight(l[t][g], m[g]);
+                        s[g] += p;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) o[g][u] = fmaf(p, y[u], o[g][u]);
                     }
                 }
             }
-            __syncwarp();  // every lane is done with the stage before the next issue refills it
-            st = st + 1 == kRing ? 0 : st + 1;
         }
-        cp_wait<0>();
-        if (bad_page) report(a.status, KVC_DEV_BAD_PAGE, row);
-        if (bad_list) report(a.status, KVC_DEV_BAD_LIST, row);
+        __syncwarp();  // every lane is done with the stage before the next issue refills it
+        st = st + 1 == kRing ? 0 : st + 1;
 
         // the row's result, or its part
-        const bool begins = off == 0, ends = off + cnt == nch, whole = begins && ends;
+        const int after = pick(b_left, i);
+        if (after > 0 && i + 1 < total) continue;
+        const bool ends = after == 0, whole = begins && ends;
         float *part = whole ? a.out + hbase * D : ends ? head_part : reinterpret_cast<float *>(ring);
         float *stat = part + G * D;
-        if (!whole && lane == 0) segs[2 * warp + (ends ? 0 : 1)] = make_int4(row, begins, ends, nch - off - cnt);
+        if (!whole && lane == 0) segs[2 * warp + (ends ? 0 : 1)] = make_int4(row, begins, ends, after);
         if constexpr (MM) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
@@ -515,37 +569,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
             }
         }
         __syncwarp();
+        row = -1;
     }
+    cp_wait<0>();
     __syncthreads();
 
-    // join the parts of each row the CTA shares
-    for (int i = 0; i < 2 * kWarps;) {
-        const int row = segs[i].x;
-        if (row < 0) {
-            ++i;
-            continue;
-        }
-        int j = i;  // the row's last part in this CTA
-        for (int k = i + 1; k < 2 * kWarps; ++k)
-            if (segs[k].x == row) j = k;
-        const bool begins = segs[i].y, ends = segs[j].z, whole = begins && ends;
+    // join the parts of each row the CTA shares; a warp's elements are of one head, lane k weighs part k
+    auto seg = [&](int k) {
+        const size_t at = (k & 1) ? (size_t)(k >> 1) * kRing * kStage : (size_t)kWarps * kRing * kStage + (size_t)(k >> 1) * rec * 4;
+        return reinterpret_cast<const float *>(smem + at);
+    };
+    const int4 mine = segs[lane % (2 * kWarps)];
+    unsigned open = __ballot_sync(0xffffffffu, lane < 2 * kWarps && mine.x >= 0);
+    while (open) {
+        const int first = __ffs(open) - 1, row = __shfl_sync(0xffffffffu, mine.x, first);
+        const unsigned group = __ballot_sync(0xffffffffu, mine.x == row) & open;
+        open &= ~group;
+        const int last = 31 - __clz(group), after = __shfl_sync(0xffffffffu, mine.w, last);
+        const bool begins = __shfl_sync(0xffffffffu, mine.y, first), ends = __shfl_sync(0xffffffffu, mine.z, last);
+        const bool whole = begins && ends;
         const int64_t hbase = (int64_t)(row / Hkv) * a.num_q_heads + (row % Hkv) * G;
         float *part = whole ? a.out + hbase * D : a.parts + (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * rec;
-        auto seg = [&](int k) {
-            return reinterpret_cast<const float *>(smem + ((k & 1) ? (size_t)(k >> 1) * kRing * kStage
-                                                                   : (size_t)kWarps * kRing * kStage + (size_t)(k >> 1) * rec * 4));
-        };
         for (int e = tid; e < G * D; e += kThreads) {
             const int g = e / D;
-            float M = -INFINITY, acc = 0.f, sum = 0.f;
-            for (int k = i; k <= j; ++k)
-                if (segs[k].x == row) M = fmaxf(M, seg(k)[G * D + 2 * g]);
-            for (int k = i; k <= j; ++k)
-                if (segs[k].x == row) {
-                    const float f = weight(seg(k)[G * D + 2 * g], M);
-                    sum += f * seg(k)[G * D + 2 * g + 1];
-                    acc += f * seg(k)[e];
-                }
+            const bool has = (group >> lane) & 1u;
+            const float m = has ? seg(lane)[G * D + 2 * g] : -INFINITY, s = has ? seg(lane)[G * D + 2 * g + 1] : 0.f;
+            const float M = warp_max(m), f = weight(m, M), sum = warp_sum(f * s);
+            float acc = 0.f;
+#pragma unroll 4
+            for (int k = first; k <= last; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, k);
+                if ((group >> k) & 1u) acc += fk * seg(k)[e];
+            }
             part[e] = whole ? ratio(acc, sum) : acc;
             if (e == g * D) {
                 if (whole) a.lse[hbase + g] = log_sum(M, sum);
@@ -554,9 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
         }
         if (begins && !ends && tid == 0) {  // the CTA's last row: where does it end?
             const int64_t next = run_start(sh, min(sh.W, (int)(blockIdx.x + 1) * sh.per_cta));
-            a.spans[blockIdx.x] = make_int2(row, run_of(sh, next + segs[j].w - 1) / sh.per_cta);
+            a.spans[blockIdx.x] = make_int2(row, run_of(sh, next + after - 1) / sh.per_cta);
         }
-        i = j + 1;
     }
 }
 
