@@ -417,6 +417,7 @@ kvc_status kvc_norm_rope_write(const kvc_cache *cache, const void *qkv, int64_t 
                     (long long)vec);
     if (((uintptr_t)qkv | (uintptr_t)q_out | (uintptr_t)q_weight | (uintptr_t)k_weight) & 15)
         return fail(KVC_ERR_INVALID_ARGUMENT, "qkv, q_out and the weights must be 16-byte aligned");
+    if ((uintptr_t)slot_map & 7) return fail(KVC_ERR_INVALID_ARGUMENT, "slot_map must be 8-byte aligned");
     return cuda_status(kvc::launch_norm_rope(c, qkv, token_stride, num_tokens, token_count, num_q_heads, q_weight,
                                              k_weight, eps, inv_freq, rope_dim, (flags & KVC_ROPE_INTERLEAVED) != 0,
                                              token_pos, slot_map, q_out, d_status, (cudaStream_t)stream),

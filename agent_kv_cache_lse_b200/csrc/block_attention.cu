@@ -8,7 +8,7 @@
 //
 // The split.  A row's slots, in list order, are cut into chunks of CH (16 at bf16, 8 at fp32), and the chunks of all
 // rows are shared out evenly over the launch's warps (rowshare.cuh).  A warp streams its run's K and V rows through a ring of
-// kRing stages of its own with 16-byte cp.async, kRing - 1 chunks ahead, and keeps a running maximum m, sum s and output o
+// stages of its own with 16-byte cp.async, one or more chunks ahead, and keeps a running maximum m, sum s and output o
 // for each head (online softmax).  A row that lies inside one run is finished by its warp.  The parts (m, s, o) of one
 // that does not are joined within the CTA through shared memory, and if the row goes on in other CTAs, the CTA leaves one
 // part in the workspace: slot 1 of the CTA where the row begins, slot 0 of the others.  A second launch, which is
@@ -36,7 +36,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRing = 3;       // stages a warp
 constexpr int kMinRun = 2;     // chunks a run, where there are that many
 constexpr int kMaxGroup = 8;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -128,6 +127,14 @@ __device__ __forceinline__ int row_slots(const AttnArgs &a, int r, bool tell) {
     return k * P - (last == nb - 1 ? nb * P - n : 0);  // only the row's last page may be partly filled
 }
 
+// Stages a warp: 16 KB of K and V, 8 KB of them in flight while the other 8 are worked on.  More in flight saturates the
+// memory system, and it then serves some SMs 25% faster than others: 3 stages of 8 KB took 229 us where 2 took 223 us
+// (16 sequences, 8K to 33K slots, 8 heads; the SMs' ends lay 60 us apart), 99.4 where 2 took 97.5 (one of 131,072 slots).
+template <typename T, int D>
+constexpr int ring_stages() {
+    return 16384 / (2 * (sizeof(T) == 2 ? 16 : 8) * D * (int)sizeof(T));
+}
+
 // out and lse of one (row, head) from a sum of weights and the weighted sum of V elements
 __device__ __forceinline__ float ratio(float acc, float sum) { return sum == 0.f ? 0.f : acc / sum; }
 __device__ __forceinline__ float log_sum(float m, float sum) { return sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLn2; }
@@ -140,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     constexpr int PC = RB / 16;                       // 16-byte pieces of a key
     constexpr uint32_t kHalf = CH * RB;               // bytes of a chunk's K (or V)
     constexpr uint32_t kStage = 2 * kHalf + CH * 4;   // K rows, V rows, positions
+    constexpr int kRing = ring_stages<T, D>();
     constexpr int NS = D / 16;
     constexpr int LK = D / 8, KW = 32 / LK, STEPS = CH / KW;  // fp32: lanes a key, keys a step
     constexpr float kSlack = 8.f;                     // bf16: the maximum moves only when a logit passes it by 8 (log2)
@@ -671,7 +679,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
 template <typename T, int D, int GM>
 cudaError_t launch_main(const AttnArgs &a, int grid, cudaStream_t stream) {
     constexpr int CH = sizeof(T) == 2 ? 16 : 8;
-    constexpr size_t kRings = (size_t)kWarps * kRing * (2 * CH * D * sizeof(T) + CH * 4);
+    constexpr size_t kRings = (size_t)kWarps * ring_stages<T, D>() * (2 * CH * D * sizeof(T) + CH * 4);
     static_assert(kRings + kWarps * kMaxGroup * (D + 2) * 4 <= 226 * 1024, "shared memory");
     const size_t bytes = kRings + (size_t)kWarps * a.group * (D + 2) * 4;
     const bool whole = a.c.page_size % CH == 0;
