@@ -3,7 +3,8 @@
 // bounds[row][b][0][d] = min k[d], bounds[row][b][1][d] = max k[d] over the row's slots in page b, exact in the cache's
 // type (a minimum rounds nothing); a NaN among the keys of an element gives NaN.  Reading K once is all there is to
 // it, so a warp takes a page: D * sizeof(T) / 16 lanes cover a key row with 16 bytes each, and the warp's key groups
-// join with shuffles at the end.
+// join with shuffles at the end.  A row's pages go round the warps of its CTAs; a warp looks its page ids up 32 at a
+// time and has the loads of the next kBatch key groups in flight while it works on the last ones.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -14,8 +15,10 @@
 namespace kvc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;  // small CTAs: after a decode step a row has a page or two to do
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtas = 8;     // a multiprocessor, at 128 registers a thread
+constexpr int kBatch = 8;  // 16-byte loads a lane has in flight (4 KB a warp)
 
 struct BoundsArgs {
     CacheView c;
@@ -42,7 +45,7 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) bounds_kernel(BoundsArgs a) {
     constexpr int N = 16 / sizeof(T), LK = D / N, ROWS = 32 / LK;
     const CacheView &c = a.c;
     const int row = blockIdx.y, lane = threadIdx.x & 31, sub = lane % LK, grp = lane / LK, P = c.page_size;
@@ -52,31 +55,78 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsArgs a) {
         return;
     }
     const int nb = (n + P - 1) / P, first = a.from_len ? max(0, a.from_len[row]) / P : 0;
-    for (int b = first + blockIdx.x * kWarps + (threadIdx.x >> 5); b < nb; b += gridDim.x * kWarps) {
-        const int64_t rb = (int64_t)row * c.max_pages_per_row + b;
-        const int32_t pg = c.block_table[rb];
-        if (pg < 0 || pg >= c.num_pages) {
+    const int b0 = first + blockIdx.x * kWarps + (threadIdx.x >> 5), stride = gridDim.x * kWarps;
+    const int mine = b0 < nb ? (nb - 1 - b0) / stride + 1 : 0;  // pages of this warp: b0, b0 + stride, ...
+    if (mine == 0) return;
+    const int32_t *bt = c.block_table + (int64_t)row * c.max_pages_per_row;
+    const int32_t *posr = c.slot_pos + (int64_t)row * c.max_slots;
+    const T *kp = static_cast<const T *>(c.k_pool) + sub * N;
+    int ids = -1, pos = INT32_MAX;
+    // the next batch to load: key groups q .. q + kBatch - 1 (ROWS keys each) of page number `i` of this warp
+    int i = 0, q = 0;
+    const T *page = nullptr;
+    int cnt = 0, low_pos = 0;
+    auto next_page = [&]() {  // skips bad pages; page is null past the last
+        for (page = nullptr; i < mine; ++i) {
+            if ((i & 31) == 0) ids = i + lane < mine ? bt[b0 + (i + lane) * stride] : -1;
+            const int32_t pg = __shfl_sync(0xffffffffu, ids, i & 31);
+            const int b = b0 + i * stride;
+            if (pg >= 0 && pg < c.num_pages) {
+                page = kp + (int64_t)pg * P * D;
+                cnt = min(P, n - b * P);  // at least 1
+                q = 0;
+                low_pos = INT32_MAX;
+                for (int s = lane; s < cnt; s += 32) low_pos = min(low_pos, posr[b * P + s]);
+                return;
+            }
             if (lane == 0) {
                 report(a.status, KVC_DEV_BAD_PAGE, row);
-                a.block_pos[rb] = INT32_MAX;
+                a.block_pos[(int64_t)row * c.max_pages_per_row + b] = INT32_MAX;
             }
-            continue;
         }
-        const int cnt = min(P, n - b * P);  // at least 1
-        const T *kp = static_cast<const T *>(c.k_pool) + (int64_t)pg * P * D + sub * N;
-        uint4 lo, hi;
-        lo = hi = *reinterpret_cast<const uint4 *>(kp + min(grp, cnt - 1) * D);  // groups past the end repeat the last key
-#pragma unroll 8
-        for (int i = grp + ROWS; i < cnt; i += ROWS) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(kp + i * D);
-            lo.x = pick<T, false>(lo.x, u.x), hi.x = pick<T, true>(hi.x, u.x);
-            lo.y = pick<T, false>(lo.y, u.y), hi.y = pick<T, true>(hi.y, u.y);
-            lo.z = pick<T, false>(lo.z, u.z), hi.z = pick<T, true>(hi.z, u.z);
-            lo.w = pick<T, false>(lo.w, u.w), hi.w = pick<T, true>(hi.w, u.w);
+    };
+    uint4 u[kBatch];
+    int groups = 0, at = 0;  // key groups in u; the page they are of
+    bool last = false;       // they end their page
+    auto load = [&]() {
+        groups = 0;
+        if (!page) return;
+        at = b0 + i * stride;
+        pos = low_pos;
+        const int all = (cnt + ROWS - 1) / ROWS;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)  // lanes past the end repeat the last key
+            if (q + k < all) u[k] = *reinterpret_cast<const uint4 *>(page + min((q + k) * ROWS + grp, cnt - 1) * D);
+        groups = min(kBatch, all - q);
+        q += kBatch;
+        last = q >= all;
+        if (last) {
+            ++i;
+            next_page();
         }
-        int pos = INT32_MAX;
-        for (int i = lane; i < cnt; i += 32) pos = min(pos, c.slot_pos[(int64_t)row * c.max_slots + b * P + i]);
-        __syncwarp();
+    };
+    next_page();
+    load();
+    uint4 lo, hi;
+    bool fresh = true;
+    while (groups > 0) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) v[k] = u[k];
+        const int have = groups, b = at, page_pos = pos;
+        const bool ends = last;
+        load();
+        if (fresh) lo = hi = v[0];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (k < have) {
+                lo.x = pick<T, false>(lo.x, v[k].x), hi.x = pick<T, true>(hi.x, v[k].x);
+                lo.y = pick<T, false>(lo.y, v[k].y), hi.y = pick<T, true>(hi.y, v[k].y);
+                lo.z = pick<T, false>(lo.z, v[k].z), hi.z = pick<T, true>(hi.z, v[k].z);
+                lo.w = pick<T, false>(lo.w, v[k].w), hi.w = pick<T, true>(hi.w, v[k].w);
+            }
+        fresh = ends;
+        if (!ends) continue;
 #pragma unroll
         for (int o = LK; o < 32; o <<= 1) {
             lo.x = pick<T, false>(lo.x, __shfl_xor_sync(0xffffffffu, lo.x, o));
@@ -88,11 +138,12 @@ __global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsArgs a) {
             hi.z = pick<T, true>(hi.z, __shfl_xor_sync(0xffffffffu, hi.z, o));
             hi.w = pick<T, true>(hi.w, __shfl_xor_sync(0xffffffffu, hi.w, o));
         }
-        pos = __reduce_min_sync(0xffffffffu, pos);
+        const int64_t rb = (int64_t)row * c.max_pages_per_row + b;
         T *out = static_cast<T *>(a.bounds) + rb * 2 * D + sub * N;
         if (grp == 0) *reinterpret_cast<uint4 *>(out) = lo;
         if (grp == ROWS - 1) *reinterpret_cast<uint4 *>(out + D) = hi;
-        if (lane == 0) a.block_pos[rb] = pos;
+        const int least = __reduce_min_sync(0xffffffffu, page_pos);
+        if (lane == 0) a.block_pos[rb] = least;
     }
 }
 
@@ -108,9 +159,9 @@ cudaError_t launch(const BoundsArgs &a, dim3 grid, cudaStream_t stream) {
 cudaError_t launch_block_bounds(const CacheView &c, const int32_t *from_len, void *bounds, int32_t *block_pos,
                                 int32_t *status, cudaStream_t stream) {
     BoundsArgs a{c, from_len, bounds, block_pos, status};
-    // a warp a page while that leaves the GPU's resident warps room, else the rows' CTAs walk their pages
+    // a warp a page while that fits the GPU at once, else the rows' CTAs walk their pages
     const int wide = (c.max_pages_per_row + kWarps - 1) / kWarps;
-    const int xb = std::max(1, std::min((device_sms() * 8 + c.rows - 1) / c.rows, wide));
+    const int xb = std::max(1, std::min(device_sms() * kCtas / c.rows, wide));
     const dim3 grid(xb, c.rows);
     return c.dtype == KVC_BF16 ? launch<__nv_bfloat16>(a, grid, stream) : launch<float>(a, grid, stream);
 }
