@@ -6,12 +6,18 @@
 // free_pages[depth - total + off_r + k].  Token t of row r then lives in slot n_r + i, whose physical slot is
 // page * P + (n_r + i) % P.
 //
-// Launch A (one CTA): exclusive scans of c_s (token_start) and need_r (off_r), the refusals, the new lengths and
-//   the new stack depth.  A thread reads a row's old length before it writes its new one, so row_len_out may be the
-//   cache's own row_len; launch B takes the old length as new length - c_s.
-// Launch B: a thread per (token, layer, head).  The thread whose slot opens a page enters that page in the block
+// The plan (one CTA): a thread takes a run of sequences and a run of rows, one scan over the CTA gives token_start and off_r,
+//   and the refusals, the new lengths and the new depth follow.  A thread reads a row's old length before it writes its
+//   new one, so row_len_out may be the cache's own row_len; the fill takes the old length as new length - c_s.
+// The fill: for every (token, layer, head) its slot.  The thread whose slot opens a page enters that page in the block
 //   table: a slot at offset 0 is past the old length only in a page the row did not hold, and nobody in this
-//   launch reads that entry (new pages come from the stack).
+//   launch reads that entry (new pages come from the stack).  A CTA takes kTile tokens of 32 rows: slot_pos, labels and crf
+//   run along a row, the slot map along the rows of a token, so lanes are tokens of a row while the former are written and
+//   the map goes through shared memory and out with lanes as rows (a thread a cell in the map's order, with
+//   scattered writes to the rows and a search of the sequence for each cell, took 28 us where this takes 6).
+// The bytes are few; what counts is the chain of dependent loads and the launches.  A decode step's few cells are
+// filled by the planning CTA itself; else the fill is a second launch that is resident before the plan ends
+// (programmatic dependent launch).
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,6 +28,8 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kFillThreads = 256;
+constexpr int kTile = 64;          // tokens a CTA of the fill takes
+constexpr int kAloneTiles = 2;     // tiles (kTile tokens of 32 rows) that the planning CTA fills itself
 
 struct ReserveArgs {
     CacheView c;
@@ -63,103 +71,143 @@ __device__ __forceinline__ int row_need(const ReserveArgs &a, int r, int *code) 
     return cdiv(n + cnt, c.page_size) - cdiv(n, c.page_size);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(ReserveArgs a) {
-    __shared__ long long red[32];
+// the sequence of token t: token_start[s] <= t < token_start[s + 1]
+__device__ __forceinline__ int sequence_of(const int32_t *token_start, int S, int t) {
+    int s = 0;
+    for (int hi = S; hi - s > 1;) {
+        const int mid = (s + hi) / 2;
+        if (token_start[mid] <= t) s = mid;
+        else hi = mid;
+    }
+    return s;
+}
+
+// Cell (token t, row r) of sequence s, whose cnt tokens begin at `start`: writes the row's arrays, returns the slot map's value
+__device__ __forceinline__ int64_t fill_cell(const ReserveArgs &a, int t, int s, int start, int cnt, int r) {
     const CacheView &c = a.c;
-    // block-wide exclusive scan of 64-bit values, carried over tiles of kPlanThreads
-    auto scan = [&](long long v, long long &carry) {
-        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-        long long x = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+    const int64_t at = a.ws[r];
+    if (at < 0) return -1;
+    const int P = c.page_size, n = a.row_len_out[r] - cnt, slot = n + t - start, lp = slot / P, first = cdiv(n, P);
+    int32_t *entry = c.block_table + (int64_t)r * c.max_pages_per_row + lp;
+    const int32_t pg = lp < first ? *entry : a.free_pages[at + lp - first];
+    const bool ok = pg >= 0 && pg < c.num_pages;
+    if (!ok) report(a.status, KVC_DEV_BAD_PAGE, r);
+    if (lp >= first && slot == lp * P) *entry = pg;
+    const int64_t ms = (int64_t)r * c.max_slots + slot;
+    c.slot_pos[ms] = a.next_pos[s] + t - start;
+    if (c.slot_label) c.slot_label[ms] = a.label;
+    if (a.crf) a.crf[ms] = 0.f;
+    return ok ? (int64_t)pg * P + slot - lp * P : -1;
+}
+
+// Fill kTile tokens from t0 on for 32 rows of their sequences from lh0 on (kThreads threads; all of them call it)
+template <int kThreads>
+__device__ __forceinline__ void fill_tile(const ReserveArgs &a, int t0, int lh0, bool refused, int total) {
+    __shared__ int seq_s[kTile], start_s[kTile], cnt_s[kTile];
+    __shared__ int64_t map_s[kTile][33];
+    const CacheView &c = a.c;
+    const int per = c.num_layers * c.num_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int here = min(kTile, a.max_tokens - t0), rows = min(32, per - lh0);
+    if (threadIdx.x < kTile && (int)threadIdx.x < here) {
+        const int t = t0 + threadIdx.x;
+        int s = -1, start = 0, cnt = 0, pos = -1;
+        if (t < total && !refused) {
+            s = sequence_of(a.token_start, c.num_seqs, t);
+            start = a.token_start[s];
+            cnt = count_of(a, s);
+            if (!bad_positions(a, s, cnt)) pos = a.next_pos[s] + t - start;
         }
-        __syncthreads();
-        if (lane == 31) red[w] = x;
-        __syncthreads();
-        long long before = 0, total = 0;
-        for (int k = 0; k < kPlanThreads / 32; ++k) {
-            if (k < w) before += red[k];
-            total += red[k];
-        }
-        const long long ex = carry + before + x - v;
-        carry += total;
-        return ex;
-    };
-    long long tokens = 0;
-    for (int s0 = 0; s0 < c.num_seqs; s0 += kPlanThreads) {
-        const int s = s0 + threadIdx.x;
-        if (s < c.num_seqs && a.new_count[s] < 0) report(a.status, KVC_DEV_BAD_LENGTH, s * c.num_layers * c.num_kv_heads);
-        const long long ex = scan(s < c.num_seqs ? count_of(a, s) : 0, tokens);
-        if (s < c.num_seqs) a.token_start[s] = (int)min(ex, (long long)a.max_tokens);
+        seq_s[threadIdx.x] = s;
+        start_s[threadIdx.x] = start;
+        cnt_s[threadIdx.x] = cnt;
+        if (lh0 == 0) a.token_pos[t] = pos;
     }
-    long long total = 0;
-    for (int r0 = 0; r0 < c.rows; r0 += kPlanThreads) {
-        const int r = r0 + threadIdx.x;
-        int need = 0, code = 0;
-        if (r < c.rows) {
-            need = row_need(a, r, &code);
-            if (need < 0) report(a.status, code, r);
-        }
-        const long long ex = scan(max(need, 0), total);
-        if (r < c.rows) a.ws[r] = need < 0 ? -1 : ex;
+    __syncthreads();
+    // a warp: 32 tokens of one row
+    for (int x = warp; x < rows * (kTile / 32); x += kThreads / 32) {
+        const int j = x % rows, i = x / rows * 32 + lane;
+        if (i >= here) continue;
+        const int s = seq_s[i];
+        map_s[i][j] = s < 0 ? -1 : fill_cell(a, t0 + i, s, start_s[i], cnt_s[i], s * per + lh0 + j);
     }
+    __syncthreads();
+    // a warp: 32 rows of one token
+    for (int i = warp; i < here; i += kThreads / 32)
+        if (lane < rows) a.slot_map[(int64_t)(t0 + i) * per + lh0 + lane] = map_s[i][lane];
+}
+
+// kAlone: the cells are few and this CTA fills them too
+template <bool kAlone>
+__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const __grid_constant__ ReserveArgs a) {
+    __shared__ long long red_t[32], red_p[32];
+    const CacheView &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, per = c.num_layers * c.num_kv_heads;
+    if constexpr (!kAlone) asm volatile("griddepcontrol.launch_dependents;");
     const long long depth = *a.free_count;
-    const bool over = tokens > a.max_tokens, refuse = over || (total > 0 && total > depth);
-    __syncthreads();  // the depth is read by everyone before thread 0 may write it (free_count_out may be free_count)
-    if (threadIdx.x == 0) {
-        if (refuse) report(a.status, over ? KVC_DEV_BAD_LENGTH : KVC_DEV_FREED_OVERFLOW, -1);
-        a.token_start[c.num_seqs] = (int)min(tokens, (long long)a.max_tokens);
-        a.ws[c.rows] = refuse ? 1 : 0;
-        *a.free_count_out = refuse ? depth : depth - total;
+    const int se = (c.num_seqs + kPlanThreads - 1) / kPlanThreads, s0 = min(c.num_seqs, tid * se), s1 = min(c.num_seqs, s0 + se);
+    const int re = (c.rows + kPlanThreads - 1) / kPlanThreads, r0 = min(c.rows, tid * re), r1 = min(c.rows, r0 + re);
+    long long tokens = 0, pages = 0;  // of this thread's sequences and rows
+    for (int s = s0; s < s1; ++s) {
+        if (a.new_count[s] < 0) report(a.status, KVC_DEV_BAD_LENGTH, s * per);
+        tokens += count_of(a, s);
     }
-    for (int r = threadIdx.x; r < c.rows; r += kPlanThreads) {
+    for (int r = r0; r < r1; ++r) {
+        int code = 0;
+        const int need = row_need(a, r, &code);
+        if (need < 0) report(a.status, code, r);
+        a.ws[r] = need < 0 ? -1 : pages;
+        pages += max(need, 0);
+    }
+    long long xt = tokens, xp = pages;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long yt = __shfl_up_sync(0xffffffffu, xt, o), yp = __shfl_up_sync(0xffffffffu, xp, o);
+        if (lane >= o) xt += yt, xp += yp;
+    }
+    if (lane == 31) red_t[w] = xt, red_p[w] = xp;
+    __syncthreads();
+    // every warp scans the warps' sums for itself
+    long long wt = red_t[lane], wp = red_p[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long yt = __shfl_up_sync(0xffffffffu, wt, o), yp = __shfl_up_sync(0xffffffffu, wp, o);
+        if (lane >= o) wt += yt, wp += yp;
+    }
+    const long long all_tokens = __shfl_sync(0xffffffffu, wt, 31), all_pages = __shfl_sync(0xffffffffu, wp, 31);
+    const long long before_t = __shfl_sync(0xffffffffu, wt, (w + 31) & 31), before_p = __shfl_sync(0xffffffffu, wp, (w + 31) & 31);
+    long long at = (w ? before_t : 0) + xt - tokens;
+    for (int s = s0; s < s1; ++s) {
+        a.token_start[s] = (int)min(at, (long long)a.max_tokens);
+        at += count_of(a, s);
+    }
+    const bool over = all_tokens > a.max_tokens, refuse = over || (all_pages > 0 && all_pages > depth);
+    // the depth was read by everyone before the barrier above, so free_count_out may be free_count
+    if (tid == 0) {
+        if (refuse) report(a.status, over ? KVC_DEV_BAD_LENGTH : KVC_DEV_FREED_OVERFLOW, -1);
+        a.token_start[c.num_seqs] = (int)min(all_tokens, (long long)a.max_tokens);
+        a.ws[c.rows] = refuse ? 1 : 0;
+        *a.free_count_out = refuse ? depth : depth - all_pages;
+    }
+    const long long base = depth - all_pages + (w ? before_p : 0) + xp - pages;
+    for (int r = r0; r < r1; ++r) {
         const bool take = !refuse && a.ws[r] >= 0;
-        if (take) a.ws[r] += depth - total;
+        if (take) a.ws[r] += base;
         const int n = c.row_len[r];
-        a.row_len_out[r] = take ? n + count_of(a, r / (c.num_layers * c.num_kv_heads)) : n;
+        a.row_len_out[r] = take ? n + count_of(a, r / per) : n;
+    }
+    if constexpr (kAlone) {
+        __syncthreads();  // what the CTA wrote above is read below
+        for (int t0 = 0; t0 < a.max_tokens; t0 += kTile)
+            for (int lh0 = 0; lh0 < per; lh0 += 32) {
+                fill_tile<kPlanThreads>(a, t0, lh0, refuse, (int)min(all_tokens, (long long)a.max_tokens));
+                __syncthreads();
+            }
     }
 }
 
-__global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(ReserveArgs a) {
-    const CacheView &c = a.c;
-    const int per = c.num_layers * c.num_kv_heads, P = c.page_size, S = c.num_seqs;
-    const int total = a.token_start[S];
-    const bool refused = a.ws[c.rows] != 0;
-    const int64_t cells = (int64_t)a.max_tokens * per;
-    for (int64_t x = (int64_t)blockIdx.x * kFillThreads + threadIdx.x; x < cells; x += (int64_t)gridDim.x * kFillThreads) {
-        const int t = (int)(x / per), lh = (int)(x % per);
-        if (t >= total || refused) {
-            a.slot_map[x] = -1;
-            if (lh == 0) a.token_pos[t] = -1;
-            continue;
-        }
-        int s = 0;  // the sequence with token_start[s] <= t < token_start[s + 1]
-        for (int hi = S; hi - s > 1;) {
-            const int mid = (s + hi) / 2;
-            if (a.token_start[mid] <= t) s = mid;
-            else hi = mid;
-        }
-        const int cnt = count_of(a, s), i = t - a.token_start[s], r = s * per + lh;
-        if (lh == 0) a.token_pos[t] = bad_positions(a, s, cnt) ? -1 : a.next_pos[s] + i;
-        const int64_t at = a.ws[r];
-        if (at < 0) {
-            a.slot_map[x] = -1;
-            continue;
-        }
-        const int n = a.row_len_out[r] - cnt, slot = n + i, lp = slot / P, first = cdiv(n, P);
-        int32_t *entry = c.block_table + (int64_t)r * c.max_pages_per_row + lp;
-        const int32_t pg = lp < first ? *entry : a.free_pages[at + lp - first];
-        const bool ok = pg >= 0 && pg < c.num_pages;
-        if (!ok) report(a.status, KVC_DEV_BAD_PAGE, r);
-        a.slot_map[x] = ok ? (int64_t)pg * P + slot % P : -1;
-        if (lp >= first && slot % P == 0) *entry = pg;
-        const int64_t ms = (int64_t)r * c.max_slots + slot;
-        c.slot_pos[ms] = a.next_pos[s] + i;
-        if (c.slot_label) c.slot_label[ms] = a.label;
-        if (a.crf) a.crf[ms] = 0.f;
-    }
+__global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const __grid_constant__ ReserveArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    fill_tile<kFillThreads>(a, blockIdx.x * kTile, blockIdx.y * 32, a.ws[a.c.rows] != 0, a.token_start[a.c.num_seqs]);
 }
 
 }  // namespace
@@ -170,13 +218,24 @@ cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const i
                            int64_t *slot_map, int64_t *ws, int32_t *status, cudaStream_t stream) {
     ReserveArgs a{c, new_count, next_pos, label, crf, free_pages, free_count, max_tokens, row_len_out, free_count_out,
                   token_start, token_pos, slot_map, ws, status};
-    reserve_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+    const int64_t tiles_t = ((int64_t)max_tokens + kTile - 1) / kTile, tiles_r = (c.num_layers * c.num_kv_heads + 31) / 32;
+    if (tiles_t * tiles_r <= kAloneTiles) {
+        reserve_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    }
+    reserve_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || max_tokens == 0) return e;
-    const int64_t cells = (int64_t)max_tokens * c.num_layers * c.num_kv_heads;
-    const int grid = (int)std::min<int64_t>((cells + kFillThreads - 1) / kFillThreads, (int64_t)device_sms() * 8);
-    reserve_fill_kernel<<<grid, kFillThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)tiles_t, (unsigned)tiles_r);
+    cfg.blockDim = dim3(kFillThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, reserve_fill_kernel, a);
 }
 
 }  // namespace kvc
