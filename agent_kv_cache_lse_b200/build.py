@@ -10,6 +10,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
+BIND = os.path.join(HERE, "_bind.so")  # csrc/bind.cpp, loaded by kvc.py
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -20,21 +21,22 @@ def sources():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
+    deps = sources() + [os.path.join(CSRC, "bind.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     deps.append(os.path.join(HERE, "..", "include", "kvc.h"))
     return all(os.path.getmtime(d) <= t for d in deps if os.path.exists(d))
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libkvc.so; returns its path."""
+    """Compile every csrc/*.cu for sm_100a and link libkvc.so, and compile _bind.so; returns the library's path."""
     if not force and up_to_date():
         return LIB
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     procs, objs = [], []
+    procs.append(("bind.cpp", _start_bind(BIND + ".tmp")))
     for src in sources():
         obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -51,7 +53,24 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
     if out.returncode != 0:
         raise RuntimeError("link failed:\n" + out.stdout)
     os.replace(tmp, LIB)
+    os.replace(BIND + ".tmp", BIND)
     return LIB
+
+
+def _start_bind(out: str):
+    """Compile csrc/bind.cpp against torch's headers and libraries (those of the interpreter that builds)."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
+           f"-I{sysconfig.get_paths()['include']}", "-o", out, os.path.join(CSRC, "bind.cpp"), f"-L{root}/lib",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{root}/lib"]
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
 
 
 def _reap(procs, verbose):

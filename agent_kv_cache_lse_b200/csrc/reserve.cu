@@ -14,7 +14,7 @@
 //   launch reads that entry (new pages come from the stack).  A CTA takes kTile tokens of 32 rows: slot_pos, labels and crf
 //   run along a row, the slot map along the rows of a token, so lanes are tokens of a row while the former are written and
 //   the map goes through shared memory and out with lanes as rows (a thread a cell in the map's order, with
-//   scattered writes to the rows and a search of the sequence for each cell, took 28 us where this takes 6).
+//   scattered writes to the rows and a search of the sequence for each cell, took 28 us where this takes 9).
 // The bytes are few; what counts is the chain of dependent loads and the launches.  A decode step's few cells are
 // filled by the planning CTA itself; else the fill is a second launch that is resident before the plan ends
 // (programmatic dependent launch).
@@ -28,8 +28,9 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kFillThreads = 256;
-constexpr int kTile = 64;          // tokens a CTA of the fill takes
-constexpr int kAloneTiles = 2;     // tiles (kTile tokens of 32 rows) that the planning CTA fills itself
+constexpr int kTile = 32;          // tokens a CTA of the fill takes
+constexpr int kStarts = 1024;      // sequences whose token_start a CTA searches in shared memory
+constexpr int kAloneTiles = 4;     // tiles (kTile tokens of 32 rows) that the planning CTA fills itself
 
 struct ReserveArgs {
     CacheView c;
@@ -103,18 +104,23 @@ __device__ __forceinline__ int64_t fill_cell(const ReserveArgs &a, int t, int s,
 // Fill kTile tokens from t0 on for 32 rows of their sequences from lh0 on (kThreads threads; all of them call it)
 template <int kThreads>
 __device__ __forceinline__ void fill_tile(const ReserveArgs &a, int t0, int lh0, bool refused, int total) {
-    __shared__ int seq_s[kTile], start_s[kTile], cnt_s[kTile];
+    __shared__ int seq_s[kTile], start_s[kTile], cnt_s[kTile], starts_s[kStarts];
     __shared__ int64_t map_s[kTile][33];
     const CacheView &c = a.c;
     const int per = c.num_layers * c.num_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int here = min(kTile, a.max_tokens - t0), rows = min(32, per - lh0);
+    const int here = min(kTile, a.max_tokens - t0), rows = min(32, per - lh0), S = c.num_seqs;
+    if (S < kStarts) {
+        for (int s = threadIdx.x; s <= S; s += kThreads) starts_s[s] = a.token_start[s];
+        __syncthreads();
+    }
+    const int32_t *starts = S < kStarts ? starts_s : a.token_start;
     if (threadIdx.x < kTile && (int)threadIdx.x < here) {
         const int t = t0 + threadIdx.x;
         int s = -1, start = 0, cnt = 0, pos = -1;
         if (t < total && !refused) {
-            s = sequence_of(a.token_start, c.num_seqs, t);
-            start = a.token_start[s];
-            cnt = count_of(a, s);
+            s = sequence_of(starts, S, t);
+            start = starts[s];
+            cnt = starts[s + 1] - start;
             if (!bad_positions(a, s, cnt)) pos = a.next_pos[s] + t - start;
         }
         seq_s[threadIdx.x] = s;

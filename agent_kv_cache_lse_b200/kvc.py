@@ -77,6 +77,11 @@ class KvcError(RuntimeError):
 
 _lib: Optional[ctypes.CDLL] = None
 
+try:
+    from . import _bind  # the ordinary case of the per-layer calls, packed natively (csrc/bind.cpp)
+except ImportError:  # not built: the same calls, packed below
+    _bind = None
+
 
 def lib() -> ctypes.CDLL:
     """Load libkvc.so from the package directory (raises if it was not built)."""
@@ -127,6 +132,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name)
             f.restype = res
             f.argtypes = args
+        if _bind is not None:
+            _bind.bind(L._handle)
         _lib = L
     return _lib
 
@@ -373,7 +380,18 @@ def kvc_step_scores(cache: Cache, scores: torch.Tensor, step_start: torch.Tensor
            "kvc_step_scores")
 
 
-# kvc_cache as bytes: the calls below are made once per layer and token, and packing is a third of the cost of a Structure
+# The calls below are made once per layer and token.  Each first tries _bind, which makes the call if every argument is as it
+# should be and returns its status, or does nothing and returns -1; what follows then checks, explains and calls.
+
+
+def _done(status: int, what: str) -> bool:
+    """Whether _bind made the call (raises if the call refused its arguments)."""
+    if status > 0:
+        _check(status, what)
+    return status == KVC_OK
+
+
+# kvc_cache as bytes: packing is a third of the cost of a Structure
 _CACHE = struct.Struct("@PPqiiiiPPPPiiii")
 assert _CACHE.size == ctypes.sizeof(KvcCache)
 _DTYPE = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}
@@ -448,6 +466,10 @@ def kvc_reserve_slots(cache: Cache, new_count: torch.Tensor, next_pos: torch.Ten
                       stream=None):
     """Slots for new_count[s] new tokens of each sequence.  token_start: [S + 1] int32; token_pos: [max_tokens] int32;
     slot_map: [max_tokens][L][Hkv] int64; row_len_out and free_count_out may be cache.row_len and free_count."""
+    if _bind is not None and _done(_bind.reserve(cache, new_count, next_pos, label, crf, free_pages, free_count,
+                                                    row_len_out, free_count_out, token_start, token_pos, slot_map,
+                                                    workspace, d_status, stream), "kvc_reserve_slots"):
+        return
     c, rows, mp, P, _, _, dev = _cache_args(cache)
     _tables(cache, rows, mp, P, dev)
     S, T = cache.num_seqs, token_pos.shape[0]
@@ -474,6 +496,9 @@ def kvc_norm_rope_write(cache: Cache, qkv: torch.Tensor, token_pos: torch.Tensor
     """Norm and rotate the query and key heads of qkv [T][L][Hq + 2 Hkv][D] (tokens may be further apart than their
     size: a slice of a wider array), queries to q_out [T][L][Hq][D], keys and values to the cache slots of slot_map
     [T][L][Hkv].  inv_freq: [rope_dim / 2] fp32 or None for no rotation; token_count: one int32, the tokens present."""
+    if _bind is not None and _done(_bind.write(cache, qkv, token_pos, slot_map, q_out, q_weight, k_weight, eps,
+                                                  inv_freq, interleaved, token_count, d_status, stream), "kvc_norm_rope_write"):
+        return
     c, _, _, _, D, dt, dev = _cache_args(cache)
     L, H = cache.num_layers, cache.num_kv_heads
     if qkv.dim() != 4 or qkv.shape[1] != L or qkv.shape[3] != D or qkv.shape[2] <= 2 * H:
@@ -503,6 +528,8 @@ def kvc_block_bounds(cache: Cache, bounds: torch.Tensor, block_pos: torch.Tensor
                      from_len: Optional[torch.Tensor] = None, d_status=None, stream=None):
     """Minimum and maximum of every page's keys: bounds [rows][max_pages][2][D] in the cache dtype, block_pos
     [rows][max_pages] int32 (lowest position); from_len [rows] int32: only the pages from that slot on."""
+    if _bind is not None and _done(_bind.bounds(cache, bounds, block_pos, from_len, d_status, stream), "kvc_block_bounds"):
+        return
     c, rows, mp, P, D, dt, dev = _cache_args(cache)
     _tables(cache, rows, mp, P, dev)
     _call("kvc_block_bounds", dev, stream, c, _opt(from_len, "from_len", (rows,), _I32, dev),
@@ -520,6 +547,9 @@ def kvc_select_blocks(cache: Cache, bounds: torch.Tensor, block_pos: torch.Tenso
     """The top_k = block_list.shape[1] pages of each row with the highest bound on the group's logits, the first
     sink_blocks and last recent_blocks always among them: block_list [rows][top_k] int32 ascending, then -1;
     block_count [rows] int32."""
+    if _bind is not None and _done(_bind.select(cache, bounds, block_pos, q, q_pos, block_list, block_count, workspace,
+                                                   sink_blocks, recent_blocks, d_status, stream), "kvc_select_blocks"):
+        return
     c, rows, mp, P, D, dt, dev = _cache_args(cache)
     _tables(cache, rows, mp, P, dev)
     S, L, Hq, k = cache.num_seqs, cache.num_layers, q.shape[2], block_list.shape[1]
@@ -541,6 +571,9 @@ def kvc_block_attention(cache: Cache, q: torch.Tensor, q_pos: torch.Tensor, out:
     """Attention of one new token over the listed pages (block_list [rows][stride] int32 ascending, block_count [rows]
     int32), or over the whole rows without a list.  q: [S][L][Hq][D] in the cache dtype; q_pos: [S] int32; out:
     [S][L][Hq][D] fp32; lse: [S][L][Hq] fp32."""
+    if _bind is not None and _done(_bind.attend(cache, q, q_pos, out, lse, workspace, block_list, block_count, d_status,
+                                                   stream), "kvc_block_attention"):
+        return
     c, rows, mp, P, D, dt, dev = _cache_args(cache)
     _tables(cache, rows, mp, P, dev)
     if (block_list is None) != (block_count is None):
