@@ -107,24 +107,21 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&w)[3]) {
     }
 }
 
-// slots of row r that take part, in list order (0 for a row whose length or list is not usable; `tell` reports it)
+// slots of row r that take part, in list order, those of a partly filled last page all counted (0 for a row whose length or
+// list is not usable; `tell` reports it)
 __device__ __forceinline__ int row_slots(const AttnArgs &a, int r, bool tell) {
     const CacheView &c = a.c;
     const int n = c.row_len[r], k = a.list ? a.list_len[r] : 0, P = c.page_size;  // one round trip for both
-    const bool in = !a.list || (k > 0 && k <= a.list_stride);
-    const int last = a.list && in ? a.list[(int64_t)r * a.list_stride + k - 1] : 0;
     if (n < 0 || n > c.max_slots) {
         if (tell) report(a.status, KVC_DEV_BAD_LENGTH, r);
         return 0;
     }
     if (!a.list) return n;
-    const int nb = (n + P - 1) / P;
-    if (k == 0) return 0;
-    if (!in || k > nb || last < 0 || last >= nb) {
+    if (k < 0 || k > a.list_stride || k > (n + P - 1) / P) {
         if (tell) report(a.status, KVC_DEV_BAD_LIST, r);
         return 0;
     }
-    return k * P - (last == nb - 1 ? nb * P - n : 0);  // only the row's last page may be partly filled
+    return k * P;
 }
 
 // Stages a warp: 16 KB of K and V, 8 KB of them in flight while the other 8 are worked on.  More in flight saturates the
@@ -215,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
         }
         slot = b * P + o;
         src = (int64_t)pg * P + o;
-        keys = min(CH, n - slot);  // the page may end behind the row's last slot
+        keys = max(0, min(CH, n - slot));  // the page may end behind the row's last slot
     };
     auto fill = [&](int base, int &brow, int &boff, int &bleft, int &bslot, int64_t &bsrc, int &bkeys) {
         const int need = min(32, total - base);
@@ -598,18 +595,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
         const bool whole = begins && ends;
         const int64_t hbase = (int64_t)(row / Hkv) * a.num_q_heads + (row % Hkv) * G;
         float *part = whole ? a.out + hbase * D : a.parts + (int64_t)(2 * blockIdx.x + (begins ? 1 : 0)) * rec;
-        for (int e = tid; e < G * D; e += kThreads) {
+        for (int e = 2 * tid; e < G * D; e += 2 * kThreads) {
             const int g = e / D;
             const bool has = (group >> lane) & 1u;
-            const float m = has ? seg(lane)[G * D + 2 * g] : -INFINITY, s = has ? seg(lane)[G * D + 2 * g + 1] : 0.f;
-            const float M = warp_max(m), f = weight(m, M), sum = warp_sum(f * s);
-            float acc = 0.f;
+            const float2 ms = has ? reinterpret_cast<const float2 *>(seg(lane) + G * D)[g] : make_float2(-INFINITY, 0.f);
+            const float M = warp_max(ms.x), f = weight(ms.x, M), sum = warp_sum(f * ms.y);
+            float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 4
             for (int k = first; k <= last; ++k) {
                 const float fk = __shfl_sync(0xffffffffu, f, k);
-                if ((group >> k) & 1u) acc += fk * seg(k)[e];
+                if ((group >> k) & 1u) {
+                    const float2 x = *reinterpret_cast<const float2 *>(seg(k) + e);
+                    acc.x += fk * x.x;
+                    acc.y += fk * x.y;
+                }
             }
-            part[e] = whole ? ratio(acc, sum) : acc;
+            part[e] = whole ? ratio(acc.x, sum) : acc.x;
+            part[e + 1] = whole ? ratio(acc.y, sum) : acc.y;
             if (e == g * D) {
                 if (whole) a.lse[hbase + g] = log_sum(M, sum);
                 else part[G * D + 2 * g] = M, part[G * D + 2 * g + 1] = sum;

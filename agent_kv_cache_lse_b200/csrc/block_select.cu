@@ -84,7 +84,7 @@ struct Element<float> {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) block_score_kernel(SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) block_score_kernel(SelectArgs a) {
     constexpr int N = 16 / sizeof(T);          // elements of a lane's load
     constexpr int LOADS = 2 * D / (32 * N) > 0 ? 2 * D / (32 * N) : 1;  // a page
     constexpr int LANES = 2 * D / (N * LOADS); // lanes that hold a page's elements (16 at bf16, D 64; else 32)

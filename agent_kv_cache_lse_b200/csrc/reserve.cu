@@ -14,7 +14,7 @@
 //   launch reads that entry (new pages come from the stack).  A CTA takes kTile tokens of 32 rows: slot_pos, labels and crf
 //   run along a row, the slot map along the rows of a token, so lanes are tokens of a row while the former are written and
 //   the map goes through shared memory and out with lanes as rows (a thread a cell in the map's order, with
-//   scattered writes to the rows and a search of the sequence for each cell, took 28 us where this takes 9).
+//   scattered writes to the rows and a search of the sequence for each cell, took 29 us where this takes 12, both under the profiler).
 // The bytes are few; what counts is the chain of dependent loads and the launches.  A decode step's few cells are
 // filled by the planning CTA itself; else the fill is a second launch that is resident before the plan ends
 // (programmatic dependent launch).
@@ -45,10 +45,14 @@ struct ReserveArgs {
     int32_t *token_start, *token_pos;
     int64_t *slot_map;
     int64_t *ws;  // [rows]: first new page's index on the stack, -1 for a refused row; [rows]: 1 when the call is refused
+    uint64_t recip;  // ceil(2^37 / page_size)
     int32_t *status;
 };
 
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+// x / page_size for 0 <= x < 2^25 (page_size <= 2^12: the error x * page_size / 2^37 stays below 1); a division by a
+// variable is 30 instructions, and three of them a cell were half of the fill's time
+__device__ __forceinline__ int page_of(const ReserveArgs &a, int x) { return (int)(((uint64_t)(uint32_t)x * a.recip) >> 37); }
+__device__ __forceinline__ int pages_for(const ReserveArgs &a, int slots) { return page_of(a, slots + a.c.page_size - 1); }
 
 // tokens sequence s brings (a negative count is reported where the scan meets it)
 __device__ __forceinline__ int count_of(const ReserveArgs &a, int s) { return max(0, a.new_count[s]); }
@@ -65,11 +69,12 @@ __device__ __forceinline__ int row_need(const ReserveArgs &a, int r, int *code) 
     if (cnt == 0) return 0;
     if (n < 0 || n > c.max_slots || bad_positions(a, s, cnt)) return *code = KVC_DEV_BAD_LENGTH, -1;
     if ((int64_t)n + cnt > c.max_slots) return *code = KVC_DEV_FREED_OVERFLOW, -1;
-    if (n % c.page_size != 0) {  // the first token joins the row's last page
-        const int32_t pg = c.block_table[(int64_t)r * c.max_pages_per_row + n / c.page_size];
+    const int held = pages_for(a, n);
+    if (held * c.page_size != n) {  // the first token joins the row's last page
+        const int32_t pg = c.block_table[(int64_t)r * c.max_pages_per_row + held - 1];
         if (pg < 0 || pg >= c.num_pages) return *code = KVC_DEV_BAD_PAGE, -1;
     }
-    return cdiv(n + cnt, c.page_size) - cdiv(n, c.page_size);
+    return pages_for(a, n + cnt) - held;
 }
 
 // the sequence of token t: token_start[s] <= t < token_start[s + 1]
@@ -83,28 +88,10 @@ __device__ __forceinline__ int sequence_of(const int32_t *token_start, int S, in
     return s;
 }
 
-// Cell (token t, row r) of sequence s, whose cnt tokens begin at `start`: writes the row's arrays, returns the slot map's value
-__device__ __forceinline__ int64_t fill_cell(const ReserveArgs &a, int t, int s, int start, int cnt, int r) {
-    const CacheView &c = a.c;
-    const int64_t at = a.ws[r];
-    if (at < 0) return -1;
-    const int P = c.page_size, n = a.row_len_out[r] - cnt, slot = n + t - start, lp = slot / P, first = cdiv(n, P);
-    int32_t *entry = c.block_table + (int64_t)r * c.max_pages_per_row + lp;
-    const int32_t pg = lp < first ? *entry : a.free_pages[at + lp - first];
-    const bool ok = pg >= 0 && pg < c.num_pages;
-    if (!ok) report(a.status, KVC_DEV_BAD_PAGE, r);
-    if (lp >= first && slot == lp * P) *entry = pg;
-    const int64_t ms = (int64_t)r * c.max_slots + slot;
-    c.slot_pos[ms] = a.next_pos[s] + t - start;
-    if (c.slot_label) c.slot_label[ms] = a.label;
-    if (a.crf) a.crf[ms] = 0.f;
-    return ok ? (int64_t)pg * P + slot - lp * P : -1;
-}
-
 // Fill kTile tokens from t0 on for 32 rows of their sequences from lh0 on (kThreads threads; all of them call it)
 template <int kThreads>
 __device__ __forceinline__ void fill_tile(const ReserveArgs &a, int t0, int lh0, bool refused, int total) {
-    __shared__ int seq_s[kTile], start_s[kTile], cnt_s[kTile], starts_s[kStarts];
+    __shared__ int seq_s[kTile], start_s[kTile], cnt_s[kTile], pos_s[kTile], starts_s[kStarts];
     __shared__ int64_t map_s[kTile][33];
     const CacheView &c = a.c;
     const int per = c.num_layers * c.num_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -126,15 +113,51 @@ __device__ __forceinline__ void fill_tile(const ReserveArgs &a, int t0, int lh0,
         seq_s[threadIdx.x] = s;
         start_s[threadIdx.x] = start;
         cnt_s[threadIdx.x] = cnt;
+        pos_s[threadIdx.x] = pos;
         if (lh0 == 0) a.token_pos[t] = pos;
     }
     __syncthreads();
-    // a warp: 32 tokens of one row
-    for (int x = warp; x < rows * (kTile / 32); x += kThreads / 32) {
-        const int j = x % rows, i = x / rows * 32 + lane;
-        if (i >= here) continue;
-        const int s = seq_s[i];
-        map_s[i][j] = s < 0 ? -1 : fill_cell(a, t0 + i, s, start_s[i], cnt_s[i], s * per + lh0 + j);
+    // a warp: 32 tokens of one row at a time; the dependent loads of all its rows go side by side
+    constexpr int kItems = 32 * (kTile / 32) / (kThreads / 32);
+    const int P = c.page_size;
+    int row[kItems], slot[kItems], first[kItems];
+    int64_t at[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int x = warp + k * (kThreads / 32), j = x % 32, i = x / 32 * 32 + lane;
+        row[k] = -1;
+        if (j < rows && i < here && seq_s[i] >= 0) {
+            row[k] = seq_s[i] * per + lh0 + j;
+            at[k] = a.ws[row[k]];
+            const int n = a.row_len_out[row[k]] - cnt_s[i];
+            slot[k] = n + t0 + i - start_s[i];
+            first[k] = pages_for(a, n);
+        }
+    }
+    int32_t page[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        if (row[k] < 0 || at[k] < 0) continue;
+        const int lp = page_of(a, slot[k]);
+        page[k] = lp < first[k] ? c.block_table[(int64_t)row[k] * c.max_pages_per_row + lp] : a.free_pages[at[k] + lp - first[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int x = warp + k * (kThreads / 32), j = x % 32, i = x / 32 * 32 + lane;
+        if (j >= rows || i >= here) continue;
+        int64_t value = -1;
+        if (row[k] >= 0 && at[k] >= 0) {
+            const int lp = page_of(a, slot[k]), o = slot[k] - lp * P;
+            const bool ok = page[k] >= 0 && page[k] < c.num_pages;
+            if (ok) value = (int64_t)page[k] * P + o;
+            else report(a.status, KVC_DEV_BAD_PAGE, row[k]);
+            if (lp >= first[k] && o == 0) c.block_table[(int64_t)row[k] * c.max_pages_per_row + lp] = page[k];
+            const int64_t ms = (int64_t)row[k] * c.max_slots + slot[k];
+            c.slot_pos[ms] = pos_s[i];
+            if (c.slot_label) c.slot_label[ms] = a.label;
+            if (a.crf) a.crf[ms] = 0.f;
+        }
+        map_s[i][j] = value;
     }
     __syncthreads();
     // a warp: 32 rows of one token
@@ -223,7 +246,7 @@ cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const i
                            int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
                            int64_t *slot_map, int64_t *ws, int32_t *status, cudaStream_t stream) {
     ReserveArgs a{c, new_count, next_pos, label, crf, free_pages, free_count, max_tokens, row_len_out, free_count_out,
-                  token_start, token_pos, slot_map, ws, status};
+                  token_start, token_pos, slot_map, ws, ((1ull << 37) + c.page_size - 1) / c.page_size, status};
     const int64_t tiles_t = ((int64_t)max_tokens + kTile - 1) / kTile, tiles_r = (c.num_layers * c.num_kv_heads + 31) / 32;
     if (tiles_t * tiles_r <= kAloneTiles) {
         reserve_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);

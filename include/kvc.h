@@ -456,8 +456,8 @@ size_t kvc_block_attention_workspace_bytes(int32_t rows, int32_t group, int32_t 
  * workspace:   kvc_block_attention_workspace_bytes(rows, group, head_dim) bytes; contents need not be kept.  Calls
  *              that may overlap on the GPU need workspaces of their own.
  * Limits:      num_q_heads / num_kv_heads <= 8.
- * Device faults: KVC_DEV_BAD_LENGTH, or KVC_DEV_BAD_LIST for a count or last entry outside the row: the row's results are
- * those of no visible slot.  KVC_DEV_BAD_LIST for another entry that is out of range or not ascending, or
+ * Device faults: KVC_DEV_BAD_LENGTH, or KVC_DEV_BAD_LIST for a count outside [0, list_stride] or above the row's pages: the
+ * row's results are those of no visible slot.  KVC_DEV_BAD_LIST for an entry that is out of range or not ascending, or
  * KVC_DEV_BAD_PAGE: that page is left out.
  * Every sum runs in a fixed order: results repeat bit for bit on the same device.
  */

@@ -486,7 +486,7 @@ def test_attention_device_faults():
         assert torch.equal(out[others], clean[0][others]) and torch.equal(lse[others], clean[1][others])
         if empty:
             assert (out[row] == 0).all() and (lse[row] == -float("inf")).all()
-    spoiled(1, [0, 3, -1], 2, True)        # the last entry is past the row
+    spoiled(1, [0, 3, -1], 2, False)       # an entry past the row
     spoiled(1, [0, 1, 2], 4, True)         # more entries than the list has
     spoiled(1, [0, 1, 2], -1, True)
     spoiled(1, [2, 2, 0], 2, False)        # the same page twice
