@@ -1,0 +1,94 @@
+"""One model step over a paged cache: new tokens into the rows, and attention of the newest token over the pages that
+matter for it.
+
+``ServingStep`` owns the buffers of such a step and enqueues, on the caller's stream:
+
+  extend:  kvc_reserve_slots -> kvc_norm_rope_write -> kvc_block_bounds (the pages that changed)
+  decode:  extend with one token for each sequence -> kvc_select_blocks -> kvc_block_attention
+
+(without a page budget, top_k = 0, decode attends to whole rows and keeps no bounds).  Nothing here computes; it allocates
+with torch and marshals arguments.  The free-page stack may be the freed list of an ``EvictionRound`` (its ``freed`` and
+``num_freed``), so that pages go round between eviction and new tokens; after a compaction, which moves entries
+between pages, call ``refresh``.  All calls take device tensors and do not synchronise, so a step can be captured into a
+CUDA graph; two graphs of one ServingStep share its buffers and must not overlap.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import kvc
+
+
+class ServingStep:
+    def __init__(self, cache: kvc.Cache, num_q_heads: int, max_tokens: int, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, top_k: int = 0, sink_blocks: int = 1, recent_blocks: int = 2,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, crf: Optional[torch.Tensor] = None):
+        """max_tokens: the most tokens one call brings; free_pages, free_count: the stack (free_count: one int64);
+        q_weight, k_weight [L][D], eps, inv_freq, interleaved: as for kvc_norm_rope_write; crf: the rows' LRFU values, which
+        new slots start at 0."""
+        self.cache, self.free_pages, self.free_count, self.crf = cache, free_pages, free_count, crf
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
+        self.inv_freq, self.interleaved = inv_freq, interleaved
+        self.top_k, self.sink_blocks, self.recent_blocks = top_k, sink_blocks, recent_blocks
+        dev, dt = cache.k_pool.device, cache.k_pool.dtype
+        S, L, H, rows, D = cache.num_seqs, cache.num_layers, cache.num_kv_heads, cache.rows, cache.k_pool.shape[2]
+        mp, i32 = cache.block_table.shape[1], torch.int32
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.zeros(shape, dtype=dtype, device=dev)
+
+        self.ones = torch.ones(S, dtype=i32, device=dev)
+        self.old_len = empty(rows, dtype=i32)
+        self.token_start, self.token_pos = empty(S + 1, dtype=i32), empty(max_tokens, dtype=i32)
+        self.slot_map = empty(max_tokens, L, H, dtype=torch.int64)
+        self.q = empty(max_tokens, L, num_q_heads, D, dtype=dt)
+        self.out, self.lse = empty(S, L, num_q_heads, D), empty(S, L, num_q_heads)
+        self.status = empty(2, dtype=i32)
+        self.reserve_ws = empty(kvc.kvc_reserve_workspace_bytes(rows) // 8, dtype=torch.int64)
+        self.attend_ws = empty(-(-kvc.kvc_block_attention_workspace_bytes(rows, num_q_heads // H, D) // 8), dtype=torch.int64)
+        if top_k:
+            self.bounds, self.block_pos = empty(rows, mp, 2, D, dtype=dt), empty(rows, mp, dtype=i32)
+            self.block_list, self.block_count = empty(rows, top_k, dtype=i32), empty(rows, dtype=i32)
+            self.select_ws = empty(kvc.kvc_select_blocks_workspace_bytes(rows, mp) // 8, dtype=torch.int64)
+            self.refresh()
+
+    def refresh(self, stream=None):
+        """Bounds of all pages (after a compaction, or when the cache was filled some other way)."""
+        if self.top_k:
+            kvc.kvc_block_bounds(self.cache, self.bounds, self.block_pos, None, self.status, stream)
+
+    def extend(self, qkv: torch.Tensor, new_count: torch.Tensor, next_pos: torch.Tensor, label: int = 0, stream=None):
+        """new_count[s] tokens of each sequence, packed in qkv [T][L][Hq + 2 Hkv][D] (T at most max_tokens; rows past
+        the last token are not read), the first at position next_pos[s].  Their queries are then in self.q."""
+        c, T = self.cache, qkv.shape[0]
+        main = stream if stream is not None else torch.cuda.current_stream(c.k_pool.device)
+        with torch.cuda.stream(main):
+            self.old_len.copy_(c.row_len)
+        kvc.kvc_reserve_slots(c, new_count, next_pos, label, self.crf, self.free_pages, self.free_count, c.row_len,
+                              self.free_count, self.token_start, self.token_pos[:T], self.slot_map[:T], self.reserve_ws,
+                              self.status, main)
+        kvc.kvc_norm_rope_write(c, qkv, self.token_pos[:T], self.slot_map[:T], self.q[:T], self.q_weight, self.k_weight,
+                                self.eps, self.inv_freq, self.interleaved, self.token_start[c.num_seqs:], self.status, main)
+        if self.top_k:
+            kvc.kvc_block_bounds(c, self.bounds, self.block_pos, self.old_len, self.status, main)
+
+    def decode(self, qkv: torch.Tensor, next_pos: torch.Tensor, label: int = 0, stream=None):
+        """One token of each sequence (qkv [S][L][Hq + 2 Hkv][D]) at position next_pos[s], and its attention over the
+        top_k pages of each row, the token's own among them: (out [S][L][Hq][D], lse [S][L][Hq])."""
+        c, S = self.cache, self.cache.num_seqs
+        main = stream if stream is not None else torch.cuda.current_stream(c.k_pool.device)
+        self.extend(qkv, self.ones, next_pos, label, main)
+        q, pages = self.q[:S], None
+        if self.top_k:
+            kvc.kvc_select_blocks(c, self.bounds, self.block_pos, q, next_pos, self.block_list, self.block_count,
+                                  self.select_ws, self.sink_blocks, self.recent_blocks, self.status, main)
+            pages = (self.block_list, self.block_count)
+        kvc.kvc_block_attention(c, q, next_pos, self.out, self.lse, self.attend_ws, *(pages or (None, None)),
+                                self.status, main)
+        return self.out, self.lse
+
+    def device_status(self):
+        return kvc.device_status(self.status)

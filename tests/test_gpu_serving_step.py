@@ -1,0 +1,196 @@
+"""The entry points of one model step run together (agent_kv_cache_lse_b200.step.ServingStep): after an eviction round, over
+many tokens, ragged prompts, on another stream, captured and replayed; everything against oracle.serve."""
+import numpy as np
+import pytest
+import torch
+
+from agent_kv_cache_lse_b200 import kvc, step, synth
+from agent_kv_cache_lse_b200.round import EvictionRound
+from oracle import serve
+from tests import helpers
+from tests.serve_cases import DT, cache_of, coords, np64, row_kv, step as half_step
+from tests.test_gpu_serve import U, check_attention, check_select
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+I32 = torch.int32
+
+
+def inv_freq(R):
+    return (10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)).float().to(DEV)
+
+
+def written(c, rows, qkv, start, counts, next_pos, old_len, w, R):
+    """The newest entries of the rows hold the normalised, rotated keys and the values of their tokens."""
+    S, L, H = c.num_seqs, c.num_layers, c.num_kv_heads
+    Hq = qkv.shape[2] - 2 * H
+    x = np64(qkv)
+    for r in rows:
+        s, l, h = coords(c, r)
+        k, v, pos = row_kv(c, r)
+        n, new = old_len[r], counts[s]
+        assert len(k) == n + new
+        at = np.arange(new) + next_pos[s]
+        np.testing.assert_array_equal(pos[n:], at)
+        t = slice(start[s], start[s] + new)
+        want, reach = serve.norm_rope(x[t, l:l + 1, Hq + h:Hq + h + 1], None if w is None else np64(w)[l:l + 1], 1e-6, at,
+                                      np64(inv_freq(R)), False)
+        tol = reach * 32 * U + np.abs(want) * half_step(c.k_pool.dtype)
+        assert (np.abs(k[n:] - want[:, 0, 0]) <= tol[:, 0, 0]).all()
+        np.testing.assert_array_equal(v[n:], x[t, l, Hq + H + h])
+
+
+def test_steps_after_an_eviction_round():
+    """A compacted cache (rows of unlike lengths), its freed pages as the stack, 40 decode steps and a ragged extension."""
+    spec = synth.batch16(num_seqs=3, num_layers=2, lo=300, hi=700)
+    w = helpers.build(spec, DEV)
+    rnd = EvictionRound(w.cache)
+    budget = torch.tensor([64, 113, 160], dtype=I32, device=DEV)
+    rnd.budget.copy_(budget)
+    rnd.run(w.queries, None, score_flags=kvc.KVC_SCORE_COMPUTE_LSE)
+    torch.cuda.synchronize()
+    assert rnd.device_status()[0] == 0
+    c, G, D = w.cache, spec.group, spec.head_dim
+    assert int(rnd.num_freed[0]) > 0
+    ones = (1 + 0.1 * torch.randn((2, D), device=DEV)).to(torch.bfloat16)
+    st = step.ServingStep(c, spec.num_q_heads, 64, rnd.freed, rnd.num_freed, top_k=5, q_weight=ones, k_weight=ones,
+                          inv_freq=inv_freq(D), crf=rnd.crf)
+    next_pos = torch.tensor(spec.ctx, dtype=I32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    rows = [0, 7, 8, 23, 31, 47]
+    depth = int(rnd.num_freed[0])
+    for i in range(40):
+        qkv = torch.randn((3, 2, spec.num_q_heads + 16, D), device=DEV, generator=gen).to(torch.bfloat16)
+        old = c.row_len.tolist()
+        out, lse = st.decode(qkv, next_pos, label=2)
+        torch.cuda.synchronize()
+        assert st.device_status()[0] == 0, st.device_status()
+        if i in (0, 1, 17, 39):
+            written(c, rows, qkv, [0, 1, 2], [1, 1, 1], next_pos.tolist(), old, ones, D)
+            q = st.q[:3]
+            fresh = torch.zeros_like(st.bounds), torch.zeros_like(st.block_pos)
+            kvc.kvc_block_bounds(c, *fresh)
+            held = (torch.arange(c.block_table.shape[1], device=DEV)[None] * 16 < c.row_len[:, None])
+            assert torch.equal(st.bounds[held], fresh[0][held]) and torch.equal(st.block_pos[held], fresh[1][held])
+            check_select(c, st.bounds, st.block_pos, q, next_pos, 5, 1, 2)
+            again = check_attention(c, q, next_pos, st.block_list, st.block_count, rows=rows)
+            assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+        next_pos += 1
+    assert (rnd.crf[0, 64:104] == 0).all() and (c.slot_label[0, 64:104] == 2).all()
+    taken = sum(-(-(int(n)) // 16) - -(-(int(n) - 40) // 16) for n in c.row_len.tolist())
+    assert int(rnd.num_freed[0]) == depth - taken
+    used = c.block_table[c.block_table >= 0]
+    assert len(torch.unique(used)) == len(used)  # no page in two places
+    counts = torch.tensor([30, 0, 17], dtype=I32, device=DEV)
+    qkv = torch.randn((50, 2, spec.num_q_heads + 16, D), device=DEV, generator=gen).to(torch.bfloat16)
+    old = c.row_len.tolist()
+    kept = st.q[47:].clone()
+    st.extend(qkv, counts, next_pos)
+    torch.cuda.synchronize()
+    assert st.device_status()[0] == 0 and torch.equal(st.q[47:], kept)
+    written(c, rows, qkv, [0, 30, 30], [30, 0, 17], next_pos.tolist(), old, ones, D)
+
+
+@pytest.mark.parametrize("top_k", [0, 4])
+def test_captured_step_replays_with_new_inputs(top_k):
+    c, free = cache_of([100, 31, 64, 7], 16, 64, "bf16", 2, 1, 2, seed=1, spare=40, extra_pages=6, device=DEV)
+    stack = free.to(DEV)
+    count = torch.tensor([len(free)], device=DEV)
+    next_pos = torch.tensor([100, 64], dtype=I32, device=DEV)
+    qkv = torch.zeros((2, 1, 8, 64), dtype=torch.bfloat16, device=DEV)
+    twin = kvc.Cache(*(t.clone() for t in (c.k_pool, c.v_pool, c.block_table, c.row_len, c.slot_pos, c.slot_label)), 2, 1, 2)
+    kw = dict(top_k=top_k, inv_freq=inv_freq(64))
+    a = step.ServingStep(c, 4, 2, stack, count, **kw)
+    b = step.ServingStep(twin, 4, 2, stack.clone(), count.clone(), **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        a.decode(qkv, next_pos)
+        next_pos += 1
+    torch.cuda.synchronize()
+    assert c.row_len.tolist() == [100, 31, 64, 7]  # capture runs nothing
+    for i in range(20):
+        x = torch.randn(qkv.shape, device=DEV, generator=torch.Generator(device=DEV).manual_seed(i)).to(torch.bfloat16)
+        qkv.copy_(x)
+        here = next_pos.clone()
+        g.replay()
+        out, lse = b.decode(x, here)
+        torch.cuda.synchronize()
+        assert a.device_status()[0] == 0 and b.device_status()[0] == 0
+        assert torch.equal(a.out, out) and torch.equal(a.lse, lse)
+    for x, y in ((c.k_pool, twin.k_pool), (c.v_pool, twin.v_pool), (c.block_table, twin.block_table),
+                 (c.row_len, twin.row_len), (c.slot_pos, twin.slot_pos), (c.slot_label, twin.slot_label)):
+        assert torch.equal(x, y)
+    assert c.row_len.tolist() == [120, 51, 84, 27]
+    check_attention(c, a.q, next_pos - 1, *((a.block_list, a.block_count) if top_k else ()))
+
+
+def test_two_steps_at_once_on_two_streams():
+    """Two caches with buffers of their own, their steps interleaved on two streams: the same results as alone."""
+    def make(seed):
+        c, free = cache_of([900, 31, 640, 70], 16, 128, "bf16", 2, 1, 2, seed=seed, spare=40, extra_pages=6, device=DEV)
+        s = step.ServingStep(c, 8, 2, free.to(DEV), torch.tensor([len(free)], device=DEV), top_k=9, inv_freq=inv_freq(128))
+        x = torch.randn((30, 2, 1, 12, 128), device=DEV, generator=torch.Generator(device=DEV).manual_seed(seed)).to(torch.bfloat16)
+        return c, s, x, torch.tensor([900, 640], dtype=I32, device=DEV)
+
+    def run(case, stream):
+        c, s, x, pos = case
+        with torch.cuda.stream(stream):
+            for i in range(30):
+                s.decode(x[i], pos)
+                pos.add_(1)
+                yield s.out.clone()
+    alone = []
+    for seed in (5, 6):
+        stream = torch.cuda.Stream()
+        case = make(seed)
+        torch.cuda.synchronize()
+        alone.append(list(run(case, stream)))
+        torch.cuda.synchronize()
+    cases, streams = [make(5), make(6)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    both = list(zip(run(cases[0], streams[0]), run(cases[1], streams[1])))
+    torch.cuda.synchronize()
+    for i in range(30):
+        assert torch.equal(both[i][0], alone[0][i]) and torch.equal(both[i][1], alone[1][i])
+    assert cases[0][1].device_status()[0] == 0 and cases[1][1].device_status()[0] == 0
+
+
+def test_binding_without_the_native_module_makes_the_same_calls(monkeypatch):
+    def go():
+        c, free = cache_of([90, 31, 64, 70], 16, 64, "f32", 2, 1, 2, seed=8, spare=9, extra_pages=3, device=DEV)
+        s = step.ServingStep(c, 4, 2, free.to(DEV), torch.tensor([len(free)], device=DEV), top_k=3, inv_freq=inv_freq(32))
+        x = torch.randn((2, 1, 8, 64), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+        s.decode(x, torch.tensor([90, 70], dtype=I32, device=DEV))
+        torch.cuda.synchronize()
+        assert s.device_status()[0] == 0
+        return s.out, s.lse, c.k_pool, c.block_table, s.block_list, s.q
+    assert kvc._bind is not None
+    native = go()
+    monkeypatch.setattr(kvc, "_bind", None)
+    for x, y in zip(native, go()):
+        assert torch.equal(x, y)
+
+
+def test_calls_the_native_module_hands_back():
+    """Refusals have their words, and tokens inside a wider array are taken, with the native module present."""
+    c, _ = cache_of([40], 16, 64, "f32", 1, 1, 1, seed=8, device=DEV)
+    q, qp = torch.randn((1, 1, 2, 64), device=DEV), torch.zeros(1, dtype=I32, device=DEV)
+    out, lse, ws = torch.zeros((1, 1, 2, 64), device=DEV), torch.zeros((1, 1, 2), device=DEV), torch.zeros(1 << 20, device=DEV)
+    with pytest.raises(kvc.KvcError, match="q: dtype"):
+        kvc.kvc_block_attention(c, q.double(), qp, out, lse, ws)
+    with pytest.raises(kvc.KvcError, match="lse: shape"):
+        kvc.kvc_block_attention(c, q, qp, out, lse[..., :1], ws)
+    with pytest.raises(kvc.KvcError, match="on cpu"):
+        kvc.kvc_block_attention(c, q, qp.cpu(), out, lse, ws)
+    with pytest.raises(kvc.KvcError, match="workspace"):
+        kvc.kvc_block_attention(c, q, qp, out, lse, ws[:4])
+    with pytest.raises(kvc.KvcError, match="block_table: shape|slot_pos: shape"):
+        kvc.kvc_block_attention(kvc.Cache(c.k_pool, c.v_pool, c.block_table, c.row_len, c.slot_pos[:, :-1].contiguous(), None, 1, 1, 1),
+                                q, qp, out, lse, ws)
+    with pytest.raises(kvc.KvcError, match="at most 8"):
+        big = torch.zeros((1, 1, 9, 64), device=DEV)
+        kvc.kvc_block_attention(c, big, qp, torch.zeros_like(big), torch.zeros((1, 1, 9), device=DEV), ws)
+    kvc.kvc_block_attention(c, q, qp, out, lse, ws, stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
