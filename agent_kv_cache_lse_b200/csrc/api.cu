@@ -364,8 +364,8 @@ kvc_status kvc_step_scores(const kvc_cache *cache, const float *scores, const in
 size_t kvc_reserve_workspace_bytes(int32_t rows) { return rows < 0 ? 0 : ((size_t)rows + 1) * sizeof(int64_t); }
 
 kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, const int32_t *next_pos, uint8_t label,
-                             float *crf, const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
-                             int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                             float *crf, const int32_t *free_pages, int64_t free_capacity, const int64_t *free_count,
+                             int32_t max_tokens, int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
                              int64_t *slot_map, void *workspace, size_t workspace_bytes, int32_t *d_status,
                              kvc_stream_t stream) {
     g_err[0] = 0;
@@ -374,14 +374,15 @@ kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, c
     if (s != KVC_OK) return s;
     if (!new_count || !next_pos || !free_pages || !free_count)
         return fail(KVC_ERR_INVALID_ARGUMENT, "new_count, next_pos, free_pages and free_count are required");
-    if (max_tokens < 0) return fail(KVC_ERR_INVALID_ARGUMENT, "max_tokens must be >= 0");
+    if (max_tokens < 0 || free_capacity < 0)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "max_tokens and free_capacity must be >= 0");
     if (!row_len_out || !free_count_out || !token_start || (max_tokens > 0 && (!token_pos || !slot_map)))
         return fail(KVC_ERR_INVALID_ARGUMENT,
                     "row_len_out, free_count_out, token_start, token_pos and slot_map are required");
     if (!workspace || workspace_bytes < kvc_reserve_workspace_bytes(c.rows) || ((uintptr_t)workspace & 7))
         return fail(KVC_ERR_INVALID_ARGUMENT, "workspace must be 8-byte aligned and at least %zu bytes",
                     kvc_reserve_workspace_bytes(c.rows));
-    return cuda_status(kvc::launch_reserve(c, new_count, next_pos, label, crf, free_pages, free_count, max_tokens,
+    return cuda_status(kvc::launch_reserve(c, new_count, next_pos, label, crf, free_pages, free_capacity, free_count, max_tokens,
                                            row_len_out, free_count_out, token_start, token_pos, slot_map,
                                            static_cast<int64_t *>(workspace), d_status, (cudaStream_t)stream),
                        "kvc_reserve_slots launch");

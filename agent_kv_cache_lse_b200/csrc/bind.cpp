@@ -193,7 +193,7 @@ PyObject *reserve(PyObject *, PyObject *const *a, Py_ssize_t n) {
     int32_t *st = c.status(a[13]);
     kvc_stream_t stream = c.stream(a[14]);
     if (!c.ok || T > INT32_MAX) return unhandled();
-    return PyLong_FromLong(f_reserve(&c.cache, cnt, next, (uint8_t)label, crf, fp, fc, (int32_t)T, len, fo, start, pos, map, ws,
+    return PyLong_FromLong(f_reserve(&c.cache, cnt, next, (uint8_t)label, crf, fp, free, fc, (int32_t)T, len, fo, start, pos, map, ws,
                                      bytes, st, stream));
 }
 

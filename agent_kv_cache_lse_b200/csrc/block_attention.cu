@@ -702,16 +702,7 @@ cudaError_t launch(const AttnArgs &a, int grid, cudaStream_t stream) {
     else if (a.group <= 4) e = launch_main<float, D, 4>(a, grid, stream);
     else e = launch_main<float, D, 8>(a, grid, stream);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid, a.group);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, a);
+    return launch_dependent(join_kernel<D>, dim3(grid, a.group), kJoinThreads, 0, stream, a);
 }
 
 }  // namespace

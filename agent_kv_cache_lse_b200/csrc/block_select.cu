@@ -354,17 +354,7 @@ cudaError_t launch_select_blocks(const CacheView &c, const void *bounds, const i
     static int done[kMaxDevices];
     e = dyn_smem_at_least(reinterpret_cast<const void *>(block_pick_kernel), bytes, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(c.rows);
-    cfg.blockDim = dim3(kPickThreads);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_pick_kernel, a);
+    return launch_dependent(block_pick_kernel, dim3(c.rows), kPickThreads, bytes, stream, a);
 }
 
 }  // namespace kvc

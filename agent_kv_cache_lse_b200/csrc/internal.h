@@ -39,6 +39,25 @@ inline cudaError_t dyn_smem_at_least(const void *kernel, size_t bytes, int *done
     return e;
 }
 
+// Launch a kernel that waits (griddepcontrol.wait) for the kernel launched before it on the stream, and may be resident
+// before that one ends (programmatic dependent launch).
+template <typename Args>
+cudaError_t launch_dependent(void (*kernel)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args &args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+    if (e != cudaSuccess) (void)cudaGetLastError();  // the next launch must not report it again
+    return e;
+}
+
 // Geometry and pointers resolved once on the host for a call.
 struct CacheView {
     const void *k_pool;
@@ -104,8 +123,8 @@ cudaError_t launch_step_scores(const CacheView &c, const float *scores, const in
                                const int32_t *num_steps, int32_t max_steps, float beta, float *out, int32_t *status,
                                cudaStream_t stream);
 cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const int32_t *next_pos, uint8_t label, float *crf,
-                           const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
-                           int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                           const int32_t *free_pages, int64_t free_capacity, const int64_t *free_count,
+                           int32_t max_tokens, int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
                            int64_t *slot_map, int64_t *ws, int32_t *status, cudaStream_t stream);
 cudaError_t launch_norm_rope(const CacheView &c, const void *qkv, int64_t token_stride, int32_t num_tokens,
                              const int32_t *token_count, int32_t num_q_heads, const void *q_weight, const void *k_weight,

@@ -38,6 +38,7 @@ struct ReserveArgs {
     uint8_t label;
     float *crf;
     const int32_t *free_pages;
+    int64_t free_capacity;
     const int64_t *free_count;
     int32_t max_tokens;
     int32_t *row_len_out;
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const __grid
         a.token_start[s] = (int)min(at, (long long)a.max_tokens);
         at += count_of(a, s);
     }
-    const bool over = all_tokens > a.max_tokens, refuse = over || (all_pages > 0 && all_pages > depth);
+    const bool over = all_tokens > a.max_tokens, short_ = depth > a.free_capacity || (all_pages > 0 && all_pages > depth), refuse = over || short_;
     // the depth was read by everyone before the barrier above, so free_count_out may be free_count
     if (tid == 0) {
         if (refuse) report(a.status, over ? KVC_DEV_BAD_LENGTH : KVC_DEV_FREED_OVERFLOW, -1);
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const __grid
     }
 }
 
-__global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const __grid_constant__ ReserveArgs a) {
+__global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(ReserveArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     fill_tile<kFillThreads>(a, blockIdx.x * kTile, blockIdx.y * 32, a.ws[a.c.rows] != 0, a.token_start[a.c.num_seqs]);
 }
@@ -242,10 +243,10 @@ __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const int32_t *next_pos, uint8_t label, float *crf,
-                           const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
-                           int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                           const int32_t *free_pages, int64_t free_capacity, const int64_t *free_count,
+                           int32_t max_tokens, int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
                            int64_t *slot_map, int64_t *ws, int32_t *status, cudaStream_t stream) {
-    ReserveArgs a{c, new_count, next_pos, label, crf, free_pages, free_count, max_tokens, row_len_out, free_count_out,
+    ReserveArgs a{c, new_count, next_pos, label, crf, free_pages, free_capacity, free_count, max_tokens, row_len_out, free_count_out,
                   token_start, token_pos, slot_map, ws, ((1ull << 37) + c.page_size - 1) / c.page_size, status};
     const int64_t tiles_t = ((int64_t)max_tokens + kTile - 1) / kTile, tiles_r = (c.num_layers * c.num_kv_heads + 31) / 32;
     if (tiles_t * tiles_r <= kAloneTiles) {
@@ -255,16 +256,7 @@ cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const i
     reserve_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)tiles_t, (unsigned)tiles_r);
-    cfg.blockDim = dim3(kFillThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, reserve_fill_kernel, a);
+    return launch_dependent(reserve_fill_kernel, dim3((unsigned)tiles_t, (unsigned)tiles_r), kFillThreads, 0, stream, a);
 }
 
 }  // namespace kvc

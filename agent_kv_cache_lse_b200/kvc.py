@@ -117,7 +117,7 @@ def lib() -> ctypes.CDLL:
             "kvc_append_tokens": (ctypes.c_int, [pc, vp, vp, vp, i32, ctypes.c_uint8, vp, vp, vp, vp, ctypes.c_size_t,
                                                  vp, vp]),
             "kvc_reserve_workspace_bytes": (ctypes.c_size_t, [i32]),
-            "kvc_reserve_slots": (ctypes.c_int, [vp, vp, vp, ctypes.c_uint8, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp,
+            "kvc_reserve_slots": (ctypes.c_int, [vp, vp, vp, ctypes.c_uint8, vp, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp,
                                                  ctypes.c_size_t, vp, vp]),
             "kvc_norm_rope_write": (ctypes.c_int, [vp, vp, i64, i32, vp, i32, vp, vp, f32, vp, i32, u32, vp, vp, vp, vp,
                                                    vp]),
@@ -480,7 +480,7 @@ def kvc_reserve_slots(cache: Cache, new_count: torch.Tensor, next_pos: torch.Ten
     ws, nbytes = _work(workspace, dev)
     _call("kvc_reserve_slots", dev, stream, c, _arg(new_count, "new_count", (S,), _I32, dev),
           _arg(next_pos, "next_pos", (S,), _I32, dev), label, _opt(crf, "crf", (rows, mp * P), _F32, dev),
-          _arg(free_pages, "free_pages", (free_pages.shape[0],), _I32, dev),
+          _arg(free_pages, "free_pages", (free_pages.shape[0],), _I32, dev), free_pages.shape[0],
           _arg(free_count, "free_count", (1,), _I64, dev), T, _arg(row_len_out, "row_len_out", (rows,), _I32, dev),
           _arg(free_count_out, "free_count_out", (1,), _I64, dev), _arg(token_start, "token_start", (S + 1,), _I32, dev),
           _arg(token_pos, "token_pos", (T,), _I32, dev),

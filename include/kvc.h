@@ -347,7 +347,7 @@ size_t kvc_reserve_workspace_bytes(int32_t rows);
  * one from the top of the free-page stack, in the order of kvc_append_tokens: row r's k-th new page is
  * free_pages[depth - total + offset_r + k], offset_r the pages all lower rows take, total the pages of the call.
  * In:   new_count, next_pos [num_seqs] int32 (next_pos: the position of the sequence's first new token);
- *       free_pages, free_count (device int64: the stack's depth); max_tokens: the size of token_pos and slot_map.
+ *       free_pages [free_capacity], free_count (device int64: the stack's depth); max_tokens: the size of token_pos and slot_map.
  * Out:  token_start  [num_seqs + 1] int32: where each sequence's tokens begin, and the number of tokens.
  *       token_pos    [max_tokens] int32: each token's position (-1 past the last token).
  *       slot_map     [max_tokens][num_layers][num_kv_heads] int64: page * page_size + offset of the token's
@@ -356,8 +356,8 @@ size_t kvc_reserve_workspace_bytes(int32_t rows);
  *       free_count_out  device int64: the new depth; may be free_count itself.
  * In/out: the cache's block_table (entries of new pages), slot_pos and slot_label (`label`), and crf
  *       ([rows][max_slots] fp32, may be NULL; 0) of the new slots.  k_pool and v_pool are not touched.
- * Device faults: more than max_tokens tokens (KVC_DEV_BAD_LENGTH, row -1) or a stack too shallow
- * (KVC_DEV_FREED_OVERFLOW, row -1) reserve nothing: row_len_out and free_count_out get the old values and the slot
+ * Device faults: more than max_tokens tokens (KVC_DEV_BAD_LENGTH, row -1), or a stack too shallow or
+ * deeper than free_capacity (KVC_DEV_FREED_OVERFLOW, row -1), reserve nothing: row_len_out and free_count_out get the old values and the slot
  * map -1 throughout.  A row is left alone and its slots are -1 when it would exceed max_slots
  * (KVC_DEV_FREED_OVERFLOW), its length is out of range or its positions would leave [0, INT32_MAX)
  * (KVC_DEV_BAD_LENGTH), or the page its first new token joins is bad (KVC_DEV_BAD_PAGE).  A negative count is
@@ -366,8 +366,8 @@ size_t kvc_reserve_workspace_bytes(int32_t rows);
  * workspace: kvc_reserve_workspace_bytes(rows) bytes; its contents need not be kept between calls.
  */
 kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, const int32_t *next_pos, uint8_t label,
-                             float *crf, const int32_t *free_pages, const int64_t *free_count, int32_t max_tokens,
-                             int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
+                             float *crf, const int32_t *free_pages, int64_t free_capacity, const int64_t *free_count,
+                             int32_t max_tokens, int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,
                              int64_t *slot_map, void *workspace, size_t workspace_bytes, int32_t *d_status,
                              kvc_stream_t stream);
 

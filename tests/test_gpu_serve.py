@@ -41,7 +41,7 @@ def words(nbytes):
 # -- slots -----------------------------------------------------------------------------------------------------------
 
 def reserve_case(lengths, counts, P, S, L, H, seed, spare=None, max_tokens=None, nxt=None, spoil=None, optional=True,
-                 in_place=False, extra_pages=None):
+                 in_place=False, extra_pages=None, deeper=0):
     c, free = cache_of(lengths, P, 64, "bf16", S, L, H, seed, spare=0, extra_pages=extra_pages or -(-max(counts + [1]) // P) + 1)
     per = L * H
     need = sum(max(0, -(-(n + max(0, counts[r // per])) // P) - -(-n // P)) for r, n in enumerate(lengths))
@@ -59,7 +59,7 @@ def reserve_case(lengths, counts, P, S, L, H, seed, spare=None, max_tokens=None,
     nxt = torch.tensor(nxt if nxt is not None else [100 * (s + 1) for s in range(S)], dtype=I32)
     total = sum(max(0, x) for x in counts)
     T = total + 2 if max_tokens is None else max_tokens
-    depth = spare
+    depth = spare + deeper
     h = lambda t: None if t is None else t.numpy()
     want = serve.reserve_slots(h(c.block_table), h(c.row_len), h(c.slot_pos), h(c.slot_label), h(crf), h(cnt), h(nxt), 2,
                                h(free), depth, T, L, H, P, c.k_pool.shape[0])
@@ -110,6 +110,8 @@ def test_reserve_in_place_many_rows_without_optional_arrays():
 def test_reserve_exact_stack_and_tokens():
     lengths, counts = [0, 16, 5, 40], [20, 3]
     assert reserve_case(lengths, counts, 16, 2, 1, 2, 8, spare=0, max_tokens=23)[0] == 0
+    got, want = reserve_case(lengths, counts, 16, 2, 1, 2, 8, deeper=1)  # a depth past the end of the stack's array
+    assert got == 5 and -1 in want["refused"]
     got, want = reserve_case(lengths, counts, 16, 2, 1, 2, 8, spare=-1)
     assert got == 5 and -1 in want["refused"]
     got, want = reserve_case(lengths, counts, 16, 2, 1, 2, 8, max_tokens=22)

@@ -24,12 +24,12 @@ def fake_cache(**kw):
 def test_reserve_refusals():
     L = kvc.lib()
 
-    def call(cache=None, cnt=F, nxt=F, fp=F, fc=F, T=4, rl=F, fo=F, ts=F, tp=F, sm=F, ws=F, nb=1 << 20):
-        return L.kvc_reserve_slots(ctypes.byref(cache or fake_cache()), cnt, nxt, 1, None, fp, fc, T, rl, fo, ts, tp, sm,
+    def call(cache=None, cnt=F, nxt=F, fp=F, cap=9, fc=F, T=4, rl=F, fo=F, ts=F, tp=F, sm=F, ws=F, nb=1 << 20):
+        return L.kvc_reserve_slots(ctypes.byref(cache or fake_cache()), cnt, nxt, 1, None, fp, cap, fc, T, rl, fo, ts, tp, sm,
                                    ws, nb, None, None)
     for name in ("cnt", "nxt", "fp", "fc", "rl", "fo", "ts", "tp", "sm", "ws"):
         assert call(**{name: None}) == BAD, name
-    assert call(T=-1) == BAD and call(nb=8) == BAD and call(ws=ctypes.c_void_p(260)) == BAD
+    assert call(T=-1) == BAD and call(cap=-1) == BAD and call(nb=8) == BAD and call(ws=ctypes.c_void_p(260)) == BAD
     assert call(cache=fake_cache(page_size=0)) == BAD and call(cache=fake_cache(num_seqs=40000)) == UNSUPPORTED
     assert call(cache=fake_cache(head_dim=96)) == UNSUPPORTED
     assert kvc.kvc_reserve_workspace_bytes(7) == 64 and kvc.kvc_reserve_workspace_bytes(-1) == 0
