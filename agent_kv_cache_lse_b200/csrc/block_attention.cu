@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     const CacheView &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.group, Hkv = c.num_kv_heads, P = c.page_size, rec = G * (D + 2);
-    asm volatile("griddepcontrol.launch_dependents;");
+    begin_dependent();
     if (tid < 2 * kWarps) segs[tid] = make_int4(-1, 0, 0, 0);
     if (tid == 0) a.spans[blockIdx.x] = make_int2(-1, 0);
     const Share sh = share_rows<kWarps>(c.rows, kMinRun, runs, [&](int r) {
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
     __shared__ float4 acc_s[SL][LANES];
     __shared__ float sum_s[SL];
     const int first = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, G = a.group, rec = G * (D + 2);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_dependent();
     const int2 span = a.spans[first];
     const int row = span.x, np = span.y - first + 1;
     if (row < 0) return;
@@ -689,8 +689,7 @@ cudaError_t launch_main(const AttnArgs &a, int grid, cudaStream_t stream) {
     static int done[2][kMaxDevices];
     cudaError_t e = dyn_smem_at_least(reinterpret_cast<const void *>(kernel), bytes, done[whole]);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, bytes, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid), kThreads, bytes, stream, a);
 }
 
 template <int D>

@@ -4,7 +4,8 @@
 // type (a minimum rounds nothing); a NaN among the keys of an element gives NaN.  Reading K once is all there is to
 // it, so a warp takes a page: D * sizeof(T) / 16 lanes cover a key row with 16 bytes each, and the warp's key groups
 // join with shuffles at the end.  A row's pages go round the warps of its CTAs; a warp looks its page ids up 32 at a
-// time and has the loads of the next kBatch key groups in flight while it works on the last ones.
+// time and streams its keys through a ring of kRing stages of shared memory (kBatch key groups each) with cp.async.  A lane
+// reads back only what it copied itself.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -17,8 +18,9 @@ namespace {
 
 constexpr int kThreads = 64;  // small CTAs: after a decode step a row has a page or two to do
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 8;     // a multiprocessor, at 128 registers a thread
-constexpr int kBatch = 8;  // 16-byte loads a lane has in flight (4 KB a warp)
+constexpr int kBatch = 8;      // 16-byte loads of a lane a stage (4 KB a warp)
+constexpr int kRing = 2;       // stages a warp
+constexpr int kCtas = 13;      // a multiprocessor, by their shared memory
 
 struct BoundsArgs {
     CacheView c;
@@ -45,8 +47,9 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, kCtas) bounds_kernel(BoundsArgs a) {
+__global__ void __launch_bounds__(kThreads) bounds_kernel(BoundsArgs a) {
     constexpr int N = 16 / sizeof(T), LK = D / N, ROWS = 32 / LK;
+    begin_dependent();
     const CacheView &c = a.c;
     const int row = blockIdx.y, lane = threadIdx.x & 31, sub = lane % LK, grp = lane / LK, P = c.page_size;
     const int n = c.row_len[row];
@@ -61,11 +64,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) bounds_kernel(BoundsArgs a) {
     const int32_t *bt = c.block_table + (int64_t)row * c.max_pages_per_row;
     const int32_t *posr = c.slot_pos + (int64_t)row * c.max_slots;
     const T *kp = static_cast<const T *>(c.k_pool) + sub * N;
-    int ids = -1, pos = INT32_MAX;
+    __shared__ uint4 ring_s[kWarps][kRing][kBatch][32];
+    uint4(*ring)[kBatch][32] = ring_s[threadIdx.x >> 5];
     // the next batch to load: key groups q .. q + kBatch - 1 (ROWS keys each) of page number `i` of this warp
-    int i = 0, q = 0;
+    int ids = -1, i = 0, q = 0, cnt = 0;
     const T *page = nullptr;
-    int cnt = 0, low_pos = 0;
     auto next_page = [&]() {  // skips bad pages; page is null past the last
         for (page = nullptr; i < mine; ++i) {
             if ((i & 31) == 0) ids = i + lane < mine ? bt[b0 + (i + lane) * stride] : -1;
@@ -75,8 +78,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) bounds_kernel(BoundsArgs a) {
                 page = kp + (int64_t)pg * P * D;
                 cnt = min(P, n - b * P);  // at least 1
                 q = 0;
-                low_pos = INT32_MAX;
-                for (int s = lane; s < cnt; s += 32) low_pos = min(low_pos, posr[b * P + s]);
                 return;
             }
             if (lane == 0) {
@@ -85,47 +86,64 @@ __global__ void __launch_bounds__(kThreads, kCtas) bounds_kernel(BoundsArgs a) {
             }
         }
     };
-    uint4 u[kBatch];
-    int groups = 0, at = 0;  // key groups in u; the page they are of
-    bool last = false;       // they end their page
-    auto load = [&]() {
-        groups = 0;
-        if (!page) return;
-        at = b0 + i * stride;
-        pos = low_pos;
-        const int all = (cnt + ROWS - 1) / ROWS;
+    // what a stage holds: key groups (0: nothing), whether they begin and end their page, and which page
+    struct Stage {
+        int groups, page;
+        bool begins, ends;
+    } held[kRing];
+    auto load = [&](int st) {
+        Stage s{0, 0, false, false};
+        if (page) {
+            const int all = (cnt + ROWS - 1) / ROWS;
+            s.page = b0 + i * stride;
+            s.begins = q == 0;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)  // lanes past the end repeat the last key
-            if (q + k < all) u[k] = *reinterpret_cast<const uint4 *>(page + min((q + k) * ROWS + grp, cnt - 1) * D);
-        groups = min(kBatch, all - q);
-        q += kBatch;
-        last = q >= all;
-        if (last) {
-            ++i;
-            next_page();
+            for (int k = 0; k < kBatch; ++k)  // lanes past the end repeat the last key
+                if (q + k < all)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&ring[st][k][lane])),
+                                 "l"(page + min((q + k) * ROWS + grp, cnt - 1) * D) : "memory");
+            s.groups = min(kBatch, all - q);
+            q += kBatch;
+            s.ends = q >= all;
+            if (s.ends) {
+                ++i;
+                next_page();
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");  // one a call, empty or not
+        return s;
     };
     next_page();
-    load();
-    uint4 lo, hi;
-    bool fresh = true;
-    while (groups > 0) {
-        uint4 v[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) v[k] = u[k];
-        const int have = groups, b = at, page_pos = pos;
-        const bool ends = last;
-        load();
-        if (fresh) lo = hi = v[0];
+    for (int st = 0; st < kRing - 1; ++st) held[st] = load(st);
+    uint4 lo, hi;
+    for (int st = 0;; st = st + 1 == kRing ? 0 : st + 1) {
+        const int to = st == 0 ? kRing - 1 : st - 1;
+        __syncwarp();  // the stage that is refilled has been read
+        const Stage s = load(to);
+        Stage now = s;
+#pragma unroll
+        for (int x = 0; x < kRing; ++x) {
+            if (x == to) held[x] = s;
+            if (x == st) now = held[x];
+        }
+        if (now.groups == 0) break;
+        const int b = now.page;
+        const bool ends = now.ends;
+        int low = INT32_MAX;
+        if (ends)
+            for (int x = lane; x < min(P, n - b * P); x += 32) low = min(low, posr[b * P + x]);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        if (now.begins) lo = hi = ring[st][0][lane];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-            if (k < have) {
-                lo.x = pick<T, false>(lo.x, v[k].x), hi.x = pick<T, true>(hi.x, v[k].x);
-                lo.y = pick<T, false>(lo.y, v[k].y), hi.y = pick<T, true>(hi.y, v[k].y);
-                lo.z = pick<T, false>(lo.z, v[k].z), hi.z = pick<T, true>(hi.z, v[k].z);
-                lo.w = pick<T, false>(lo.w, v[k].w), hi.w = pick<T, true>(hi.w, v[k].w);
+            if (k < now.groups) {
+                const uint4 v = ring[st][k][lane];
+                lo.x = pick<T, false>(lo.x, v.x), hi.x = pick<T, true>(hi.x, v.x);
+                lo.y = pick<T, false>(lo.y, v.y), hi.y = pick<T, true>(hi.y, v.y);
+                lo.z = pick<T, false>(lo.z, v.z), hi.z = pick<T, true>(hi.z, v.z);
+                lo.w = pick<T, false>(lo.w, v.w), hi.w = pick<T, true>(hi.w, v.w);
             }
-        fresh = ends;
         if (!ends) continue;
 #pragma unroll
         for (int o = LK; o < 32; o <<= 1) {
@@ -142,16 +160,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) bounds_kernel(BoundsArgs a) {
         T *out = static_cast<T *>(a.bounds) + rb * 2 * D + sub * N;
         if (grp == 0) *reinterpret_cast<uint4 *>(out) = lo;
         if (grp == ROWS - 1) *reinterpret_cast<uint4 *>(out + D) = hi;
-        const int least = __reduce_min_sync(0xffffffffu, page_pos);
-        if (lane == 0) a.block_pos[rb] = least;
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (lane == 0) a.block_pos[rb] = low;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename T>
 cudaError_t launch(const BoundsArgs &a, dim3 grid, cudaStream_t stream) {
-    if (a.c.head_dim == 128) bounds_kernel<T, 128><<<grid, kThreads, 0, stream>>>(a);
-    else bounds_kernel<T, 64><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(a.c.head_dim == 128 ? bounds_kernel<T, 128> : bounds_kernel<T, 64>, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_score_kernel(SelectArgs
     constexpr int BATCH = kPages / LOADS * SIDE;  // pages a warp takes at a time: 4, 8 or (fp32, D 128) 2
     constexpr int DEEP = BATCH / SIDE;         // of them in the same lanes
     __shared__ double w[2 * D];                // [down | up]
-    asm volatile("griddepcontrol.launch_dependents;");
+    begin_dependent();
     const CacheView &c = a.c;
     const int row = blockIdx.y, lane = threadIdx.x & 31, P = c.page_size, Hkv = c.num_kv_heads;
     const int seq = row / (c.num_layers * Hkv), G = a.num_q_heads / Hkv;
@@ -184,10 +184,10 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
     extern __shared__ unsigned long long cache[];
     const CacheView &c = a.c;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = c.page_size;
+    begin_dependent();
     int n = c.row_len[row];
     if (n < 0 || n > c.max_slots) n = 0;
     const int nb = (n + P - 1) / P;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const unsigned long long *keys = a.keys + (int64_t)row * c.max_pages_per_row;
     int32_t *list = a.block_list + (int64_t)row * a.top_k;
     // what there is: pages that can be taken, that always are, and the range of the others' keys
@@ -328,9 +328,8 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
 }
 
 template <typename T>
-void score(const SelectArgs &a, dim3 grid, cudaStream_t stream) {
-    if (a.c.head_dim == 128) block_score_kernel<T, 128><<<grid, kThreads, 0, stream>>>(a);
-    else block_score_kernel<T, 64><<<grid, kThreads, 0, stream>>>(a);
+cudaError_t score(const SelectArgs &a, dim3 grid, cudaStream_t stream) {
+    return launch_dependent(a.c.head_dim == 128 ? block_score_kernel<T, 128> : block_score_kernel<T, 64>, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -346,9 +345,7 @@ cudaError_t launch_select_blocks(const CacheView &c, const void *bounds, const i
     // 4 layers: 107 us with the first rule alone, 102 / 92 / 91 us with at most 4 / 8 / 16 batches)
     const int wide = (c.max_pages_per_row + kWarps * kPages - 1) / (kWarps * kPages);
     const dim3 grid(std::max(std::min(device_sms() * kCtas / c.rows, wide), (wide + 15) / 16), c.rows);
-    if (c.dtype == KVC_BF16) score<__nv_bfloat16>(a, grid, stream);
-    else score<float>(a, grid, stream);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = c.dtype == KVC_BF16 ? score<__nv_bfloat16>(a, grid, stream) : score<float>(a, grid, stream);
     if (e != cudaSuccess) return e;
     const size_t bytes = (size_t)std::min(c.max_pages_per_row, kCached) * sizeof(unsigned long long);
     static int done[kMaxDevices];

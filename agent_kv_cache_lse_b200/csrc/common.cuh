@@ -10,6 +10,13 @@ namespace kvc {
 
 constexpr int kWarp = 32;
 
+// First statement of a kernel launched with launch_dependent(): lets the next such launch become resident, and waits until
+// the kernels before this one on the stream have ended and their writes are visible.  Every CTA executes it before it
+// touches memory, so that the end of a kernel means the end of all before it.
+__device__ __forceinline__ void begin_dependent() {
+    asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
+}
+
 // First device error wins: status[0] = code, status[1] = row.
 __device__ __forceinline__ void report(int32_t *status, int code, int row) {
     if (status == nullptr) return;

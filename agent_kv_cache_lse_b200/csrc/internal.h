@@ -39,8 +39,8 @@ inline cudaError_t dyn_smem_at_least(const void *kernel, size_t bytes, int *done
     return e;
 }
 
-// Launch a kernel that waits (griddepcontrol.wait) for the kernel launched before it on the stream, and may be resident
-// before that one ends (programmatic dependent launch).
+// Launch a kernel that begins with begin_dependent() (common.cuh): it may be resident before the kernel launched before it on
+// the stream ends (programmatic dependent launch), which hides its launch.
 template <typename Args>
 cudaError_t launch_dependent(void (*kernel)(Args), dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args &args) {
     cudaLaunchAttribute attr{};

@@ -115,7 +115,8 @@ struct Place {
 };
 
 template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(NormRopeArgs a) {
+    begin_dependent();
     constexpr int N = Vec<T>::N, PV = D / N, LK = PV / 2, VW = 32 / LK;  // elements a piece; pieces, lanes a vector; vectors a step
     extern __shared__ __align__(16) unsigned char smem[];
     const CacheView &c = a.c;
@@ -303,8 +304,7 @@ cudaError_t launch_kind(const NormRopeArgs &a, cudaStream_t stream) {
     const size_t bytes = (size_t)kWarps * kWarpBytes;
     cudaError_t e = dyn_smem_at_least(reinterpret_cast<const void *>(norm_rope_kernel<T, D, kInter>), bytes, done);
     if (e != cudaSuccess) return e;
-    norm_rope_kernel<T, D, kInter><<<grid, kThreads, bytes, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(norm_rope_kernel<T, D, kInter>, dim3(grid), kThreads, bytes, stream, a);
 }
 
 template <typename T>

@@ -168,11 +168,11 @@ __device__ __forceinline__ void fill_tile(const ReserveArgs &a, int t0, int lh0,
 
 // kAlone: the cells are few and this CTA fills them too
 template <bool kAlone>
-__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const __grid_constant__ ReserveArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 1) reserve_plan_kernel(ReserveArgs a) {
     __shared__ long long red_t[32], red_p[32];
     const CacheView &c = a.c;
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, per = c.num_layers * c.num_kv_heads;
-    if constexpr (!kAlone) asm volatile("griddepcontrol.launch_dependents;");
+    begin_dependent();
     const long long depth = *a.free_count;
     const int se = (c.num_seqs + kPlanThreads - 1) / kPlanThreads, s0 = min(c.num_seqs, tid * se), s1 = min(c.num_seqs, s0 + se);
     const int re = (c.rows + kPlanThreads - 1) / kPlanThreads, r0 = min(c.rows, tid * re), r1 = min(c.rows, r0 + re);
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const __grid
 }
 
 __global__ void __launch_bounds__(kFillThreads) reserve_fill_kernel(ReserveArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_dependent();
     fill_tile<kFillThreads>(a, blockIdx.x * kTile, blockIdx.y * 32, a.ws[a.c.rows] != 0, a.token_start[a.c.num_seqs]);
 }
 
@@ -250,11 +250,9 @@ cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const i
                   token_start, token_pos, slot_map, ws, ((1ull << 37) + c.page_size - 1) / c.page_size, status};
     const int64_t tiles_t = ((int64_t)max_tokens + kTile - 1) / kTile, tiles_r = (c.num_layers * c.num_kv_heads + 31) / 32;
     if (tiles_t * tiles_r <= kAloneTiles) {
-        reserve_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
-        return cudaGetLastError();
+        return launch_dependent(reserve_plan_kernel<true>, dim3(1), kPlanThreads, 0, stream, a);
     }
-    reserve_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_dependent(reserve_plan_kernel<false>, dim3(1), kPlanThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
     return launch_dependent(reserve_fill_kernel, dim3((unsigned)tiles_t, (unsigned)tiles_r), kFillThreads, 0, stream, a);
 }
