@@ -438,7 +438,7 @@ kvc_status kvc_block_bounds(const kvc_cache *cache, const int32_t *from_len, voi
 }
 
 size_t kvc_select_blocks_workspace_bytes(int32_t rows, int32_t max_pages_per_row) {
-    return rows < 0 || max_pages_per_row < 0 ? 0 : (size_t)rows * (size_t)max_pages_per_row * sizeof(uint64_t);
+    return rows < 0 || max_pages_per_row < 0 ? 0 : kvc::select_blocks_workspace(rows, max_pages_per_row);
 }
 
 kvc_status kvc_select_blocks(const kvc_cache *cache, const void *bounds, const int32_t *block_pos, const void *q,

@@ -133,6 +133,7 @@ cudaError_t launch_norm_rope(const CacheView &c, const void *qkv, int64_t token_
                              cudaStream_t stream);
 cudaError_t launch_block_bounds(const CacheView &c, const int32_t *from_len, void *bounds, int32_t *block_pos,
                                 int32_t *status, cudaStream_t stream);
+size_t select_blocks_workspace(int64_t rows, int64_t max_pages);
 cudaError_t launch_select_blocks(const CacheView &c, const void *bounds, const int32_t *block_pos, const void *q,
                                  const int32_t *q_pos, int32_t num_q_heads, int32_t top_k, int32_t sink, int32_t recent,
                                  int32_t *block_list, int32_t *block_count, void *ws, int32_t *status,
