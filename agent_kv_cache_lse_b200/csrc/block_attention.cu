@@ -161,17 +161,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     const Share sh = share_rows<kWarps>(c.rows, kMinRun, runs, [&](int r) {
         return (row_slots(a, r, blockIdx.x == 0) + CH - 1) / CH;
     });
-    // rows without slots are answered here, a thread a row to look and a warp a row to write
-    for (int r0 = blockIdx.x * kThreads + warp * 32; r0 < c.rows; r0 += gridDim.x * kThreads) {
-        unsigned empty = __ballot_sync(0xffffffffu, r0 + lane < c.rows && row_slots(a, r0 + lane, false) == 0);
-        for (; empty; empty &= empty - 1) {
-            const int r = r0 + __ffs(empty) - 1;
-            const int64_t head = (int64_t)(r / Hkv) * a.num_q_heads + (r % Hkv) * G;
-            for (int e = lane; e < G * D; e += 32) a.out[head * D + e] = 0.f;
-            if (lane < G) a.lse[head + lane] = -INFINITY;
-        }
-    }
-
     unsigned char *ring = smem + (size_t)warp * kRing * kStage;
     const T *kp = static_cast<const T *>(c.k_pool);
     const T *vp = static_cast<const T *>(c.v_pool);
@@ -323,6 +312,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     };
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) ok[i] = issue(i, i);
+
+    // while the first chunks come: rows without slots, a thread a row to look and a warp a row to write
+    for (int r0 = blockIdx.x * kThreads + warp * 32; r0 < c.rows; r0 += gridDim.x * kThreads) {
+        unsigned empty = __ballot_sync(0xffffffffu, r0 + lane < c.rows && row_slots(a, r0 + lane, false) == 0);
+        for (; empty; empty &= empty - 1) {
+            const int r = r0 + __ffs(empty) - 1;
+            const int64_t head = (int64_t)(r / Hkv) * a.num_q_heads + (r % Hkv) * G;
+            for (int e = lane; e < G * D; e += 32) a.out[head * D + e] = 0.f;
+            if (lane < G) a.lse[head + lane] = -INFINITY;
+        }
+    }
 
     // bf16: a lane holds heads hm = 2 (lane % 4) and hm + 1; O[d][h] for d = 16 t + lane / 4 (+ 8).  fp32: a lane holds
     // elements d0 .. d0 + 3 and D / 2 + d0 .. + 3 of every head
@@ -630,44 +630,45 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a) {
     constexpr int LANES = D / 4, SL = kJoinThreads / LANES;
     __shared__ float4 acc_s[SL][LANES];
-    __shared__ float sum_s[SL];
-    const int first = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, lane = tid & 31, G = a.group, rec = G * (D + 2);
+    __shared__ float sum_s[SL], max_s[SL];
+    const int first = blockIdx.x, g = blockIdx.y, tid = threadIdx.x, G = a.group, rec = G * (D + 2);
     begin_dependent();
     const int2 span = a.spans[first];
     const int row = span.x, np = span.y - first + 1;
     if (row < 0) return;
     const int64_t head = (int64_t)(row / a.c.num_kv_heads) * a.num_q_heads + (row % a.c.num_kv_heads) * G + g;
     auto part = [&](int j) { return a.parts + (int64_t)(2 * (first + j) + (j == 0 ? 1 : 0)) * rec; };
-    float M = -INFINITY;  // every warp finds it for itself
-    for (int j = lane; j < np; j += 32) M = fmaxf(M, part(j)[G * D + 2 * g]);
-    M = warp_max(M);
     const int d = tid % LANES, sl = tid / LANES;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+    float sum = 0.f, m = -INFINITY;  // relative to the largest maximum of this thread's parts so far
 #pragma unroll 4
     for (int j = sl; j < np; j += SL) {
         const float *p = part(j);
         const float2 ms = *reinterpret_cast<const float2 *>(p + G * D + 2 * g);
         const float2 x = reinterpret_cast<const float2 *>(p + g * D)[2 * d], y = reinterpret_cast<const float2 *>(p + g * D)[2 * d + 1];
-        const float f = weight(ms.x, M);
-        sum += f * ms.y;
-        acc.x += f * x.x;
-        acc.y += f * x.y;
-        acc.z += f * y.x;
-        acc.w += f * y.y;
+        const float top = fmaxf(m, ms.x), old = weight(m, top), f = weight(ms.x, top);
+        m = top;
+        sum = sum * old + f * ms.y;
+        acc.x = acc.x * old + f * x.x;
+        acc.y = acc.y * old + f * x.y;
+        acc.z = acc.z * old + f * y.x;
+        acc.w = acc.w * old + f * y.y;
     }
     acc_s[sl][d] = acc;
-    if (d == 0) sum_s[sl] = sum;
+    if (d == 0) sum_s[sl] = sum, max_s[sl] = m;
     __syncthreads();
     if (sl == 0) {
+        float M = -INFINITY;
+        for (int k = 0; k < SL; ++k) M = fmaxf(M, max_s[k]);
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
         sum = 0.f;
         for (int k = 0; k < SL; ++k) {
-            acc.x += acc_s[k][d].x;
-            acc.y += acc_s[k][d].y;
-            acc.z += acc_s[k][d].z;
-            acc.w += acc_s[k][d].w;
-            sum += sum_s[k];
+            const float f = weight(max_s[k], M);
+            acc.x += f * acc_s[k][d].x;
+            acc.y += f * acc_s[k][d].y;
+            acc.z += f * acc_s[k][d].z;
+            acc.w += f * acc_s[k][d].w;
+            sum += f * sum_s[k];
         }
         float *out = a.out + head * D + 4 * d;
         out[0] = ratio(acc.x, sum);

@@ -7,26 +7,33 @@
 
 namespace kvc {
 
-// per_cta runs for each CTA of the launch (consecutive ones), W in all; every run has at least one unit
+// per_cta runs for each CTA of the launch (consecutive ones), W in all; every run has at least one unit: the first `more` runs
+// have each + 1, the others each.  (One division a share: U w / W for each of a CTA's runs took longer than the search.)
 struct Share {
-    int64_t U;
-    int per_cta, W;
+    int64_t U, each;
+    int per_cta, W, more;
 };
 
 // first unit of run w
-__device__ __forceinline__ int64_t run_start(const Share &s, int w) { return s.U * w / s.W; }
+__device__ __forceinline__ int64_t run_start(const Share &s, int w) { return s.each * w + min(w, s.more); }
 
-// run of unit x: the last w with U w / W <= x
-__device__ __forceinline__ int run_of(const Share &s, int64_t x) { return (int)(((x + 1) * s.W - 1) / s.U); }
+// run of unit x
+__device__ __forceinline__ int run_of(const Share &s, int64_t x) {
+    const int64_t first = (s.each + 1) * s.more;  // units of the longer runs
+    return x < first ? (int)(x / (s.each + 1)) : s.more + (int)((x - first) / s.each);
+}
 
 // A run of at least min_run units where there are that many, and at most kRuns runs a CTA
 template <int kRuns>
 __device__ __forceinline__ Share share_units(int64_t U, int ctas, int min_run) {
-    const int64_t span = (int64_t)ctas * min_run, per = (U + span - 1) / span;
     Share s;
     s.U = U;
-    s.per_cta = (int)(per < 1 ? 1 : per > kRuns ? kRuns : per);
+    const int64_t enough = (int64_t)ctas * min_run * (kRuns - 1);  // beyond this every run of every CTA is used
+    s.per_cta = U > enough ? kRuns : max(1, (int)(((unsigned)U + ctas * min_run - 1) / (unsigned)(ctas * min_run)));
     s.W = (int)min(U, (int64_t)ctas * s.per_cta);
+    if (s.W == 0) s.each = s.more = 0;
+    else if (U <= INT32_MAX) s.each = (unsigned)U / (unsigned)s.W, s.more = (int)((unsigned)U - (unsigned)s.each * (unsigned)s.W);
+    else s.each = U / s.W, s.more = (int)(U - s.each * s.W);
     return s;
 }
 
