@@ -18,10 +18,13 @@
 //
 // bf16: the chunk's two contractions are warp-level tensor-core tiles (m16n8k16, fp32 accumulate), S = K Q^T with the 16 keys
 // as rows and the heads (padded to 8) as columns, O^T += V^T P with D as rows.  P is split into three bf16 parts whose sum
-// keeps 24 bits, all of fp32's: two parts (16 bits) left the fp32 output 5e-6 off where the plain form is 4e-7 off.
+// keeps 24 bits, all of fp32's; two would keep 16, and the output is fp32.
 // A tensor-core step truncates when it adds to its accumulator, which over a run of hundreds of chunks drifts (7e-6 at 138
 // chunks), so each chunk's product starts from zero and is added to the run's output by a rounded fp32 addition.
 // fp32: a lane owns 8 elements of D of a key and all dot products are fp32 FMAs.
+// Measured (bf16, 8 KV heads, 4 query heads each): 219 us for 16 sequences of 8K to 33K slots (1.39 GB, 6.3 TB/s), 94 us for one of
+// 131,072, 35 us for 128 chosen pages of 16 sequences (136 MB): about 7 us pass before the first chunk is there, 5 at the end for
+// the joins, and the SMs end up to 10% apart.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -8,9 +8,9 @@
 // A bound that is not finite always makes the sum NaN or +inf (0 * inf, or inf - inf, where the factors' signs do
 // not), and NaN ranks as +inf.
 //
-// 64-bit arithmetic for every page took 80 instructions a page and lane and 1.4 times the time of the bytes (the conversions
-// more than the multiply-adds).  But only pages at the border need it.  With x in 32 bits, of 8 multiply-adds a lane and
-// 5 sums across lanes on factors rounded once, |x - score| <= e = 2^-20 M U, where M bounds |lo| and |hi| over the row and
+// 64-bit arithmetic for every page took 80 instructions a page and warp and 1.4 times the time of the bytes.  But only pages
+// at the border need it.  With x in 32 bits, of 8 multiply-adds a lane and 5 sums across lanes on factors rounded once (14
+// roundings of at most 2^-24 each, of sums of magnitudes), |x - score| <= e = 2^-20 M U, where M bounds |lo| and |hi| over the row and
 // U = sum_d up_d - down_d.  If c is the k-th largest x, a page above c + 2 e has a score above those of all but fewer than
 // k pages and is taken, one below c - 2 e is not, and the pages between are ranked by their scores in 64 bits: mostly there is one
 // page between, and nothing to rank.
@@ -24,6 +24,8 @@
 //   digit in which the k-th key lies, usually with a handful of keys, which are ranked directly; while there are more than
 //   kFew, the next 11 bits follow.  The 64-bit scores between c - 2 e and c + 2 e, if they have to be ranked, go the same
 //   way.  One pass in index order then lists the pages.
+// Measured: 78 us for 677,000 pages of 512 rows (16 sequences of 8K to 33K tokens, 4 layers; 62 us launch A, 5.6 TB/s), 89 us with
+// 64-bit scores throughout; 11 us for 8 rows of 2,048 pages, of which the bytes are 1.3 (a dozen barriers of launch B the rest).
 #include <cuda_bf16.h>
 
 #include <algorithm>

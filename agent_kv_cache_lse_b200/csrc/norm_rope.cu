@@ -14,14 +14,16 @@
 //     out_e = rsqrt(mean(x^2) + eps) * (C_e x_e + S_e x_p),    C_e = w_e cos f, S_e = -+ w_p sin f,  p the partner of e
 // (C = w, S = 0 past rope_dim): two multiply-adds an element and one product, in pairs (f32x2).
 // A lane takes two 16-byte pieces of a head vector, an element and its partner both (pieces p and p + rope_dim / 2; past
-// rope_dim, and when interleaved, neighbours), so that no lane needs another's elements: with one piece a lane and the
-// partner's loaded beside it a vector took three times the instructions.  A warp takes 2 to 8 vectors a step, and a lane always has
+// rope_dim, and when interleaved, neighbours), so that no lane needs another's elements (one piece a lane, and
+// the partner's loaded and converted beside it, took 28 M warp instructions for 8,192 tokens where this takes 21 M).  A warp takes
+// 2 to 8 vectors a step, and a lane always has
 // the same elements: its C and S are the same for all query heads, or all key heads, of a token and layer.  The steps of
 // all tokens (each token's layers, and in them the queries, then the keys and values) form one sequence that is cut into equal runs, one a
 // warp.  A warp takes its run in groups of up to kSteps steps of one kind, streamed through a ring of kRing stages of its
 // own with cp.async (a lane's registers then hold no loads in flight: with batches of loads in registers the kernel was
 // bound by occupancy or by spills).  When it comes to a new token it makes that token's rope_dim / 2 pairs (cos, sin) in
-// shared memory, and at a layer's queries and keys its C and S.
+// shared memory, and at a layer's queries and keys its C and S.  Measured: 148 us for 32,768 tokens of 32 + 2 x 8 heads of 128 (bf16,
+// 5.4 TB/s read and written, 57% of the issue slots), 3.9 us for 16 tokens, 10.6 us for 1,003 fp32 tokens of two layers (37 MB).
 #include <cuda_bf16.h>
 
 #include <algorithm>

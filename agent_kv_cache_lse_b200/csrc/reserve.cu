@@ -17,7 +17,8 @@
 //   scattered writes to the rows and a search of the sequence for each cell, took 29 us where this takes 12, both under the profiler).
 // The bytes are few; what counts is the chain of dependent loads and the launches.  A decode step's few cells are
 // filled by the planning CTA itself; else the fill is a second launch that is resident before the plan ends
-// (programmatic dependent launch).
+// (programmatic dependent launch).  Measured: 5.1 us for a decode step of 16 sequences (128 rows), 13 us for 28,049 prompt tokens of
+// 33 sequences in 1,056 rows (15.8 MB written, 2.4 us of them by bandwidth; the plan's and the fill's load chains are the rest).
 #include <algorithm>
 
 #include "common.cuh"
@@ -51,7 +52,7 @@ struct ReserveArgs {
 };
 
 // x / page_size for 0 <= x < 2^25 (page_size <= 2^12: the error x * page_size / 2^37 stays below 1); a division by a
-// variable is 30 instructions, and three of them a cell were half of the fill's time
+// variable is 30 instructions, and three of them a cell were a quarter of the fill's time
 __device__ __forceinline__ int page_of(const ReserveArgs &a, int x) { return (int)(((uint64_t)(uint32_t)x * a.recip) >> 37); }
 __device__ __forceinline__ int pages_for(const ReserveArgs &a, int slots) { return page_of(a, slots + a.c.page_size - 1); }
 
