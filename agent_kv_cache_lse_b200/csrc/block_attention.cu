@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
         }
         if (begins && !ends && tid == 0) {  // the CTA's last row: where does it end?
             const int64_t next = run_start(sh, min(sh.W, (int)(blockIdx.x + 1) * sh.per_cta));
-            a.spans[blockIdx.x] = make_int2(row, run_of(sh, next + after - 1) / sh.per_cta);
+            a.spans[blockIdx.x] = make_int2(row, min((int)gridDim.x - 1, run_of(sh, next + after - 1) / sh.per_cta));
         }
     }
 }

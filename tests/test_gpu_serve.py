@@ -506,3 +506,82 @@ def test_attention_device_faults():
     c.row_len[3] = 10**6
     out, lse, st = attend(c, q, qp)
     assert code(st) == 2 and (out[3] == 0).all() and (lse[3] == -float("inf")).all()
+
+
+def test_pools_past_32_bit_offsets():
+    """Pages above element 2^31 of the pool: every entry point gives what it gives on a small pool."""
+    lengths, P, D = [300, 77, 0, 1000], 16, 128
+    c, _ = cache_of(lengths, P, D, "bf16", 2, 1, 2, seed=11, device=DEV)
+    n = c.k_pool.shape[0]
+    shift = (1 << 31) // (P * D) + 5
+    big = torch.empty((shift + n, P, D), dtype=torch.bfloat16, device=DEV)  # keys and values share it: 4.3 GB
+    big[shift:] = c.k_pool
+    far = kvc.Cache(big, big, torch.where(c.block_table >= 0, c.block_table + shift, -1), c.row_len, c.slot_pos, None, 2, 1, 2)
+    near = kvc.Cache(c.k_pool, c.k_pool, c.block_table, c.row_len, c.slot_pos, None, 2, 1, 2)
+    q = torch.randn((2, 1, 8, D), device=DEV).to(torch.bfloat16)
+    qp = torch.full((2,), 2**31 - 1, dtype=I32, device=DEV)
+    li, m = a_list(c, 9, 1)
+    got = []
+    for x in (near, far):
+        st = status()
+        b = torch.zeros((4, c.block_table.shape[1], 2, D), dtype=torch.bfloat16, device=DEV)
+        pos = torch.zeros(c.block_table.shape, dtype=I32, device=DEV)
+        kvc.kvc_block_bounds(x, b, pos, None, st)
+        assert code(st) == 0
+        out = attend(x, q, qp)
+        some = attend(x, q, qp, li, m)
+        assert code(out[2]) == 0 and code(some[2]) == 0
+        got.append([b, pos, *out[:2], *some[:2]])
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    qkv = torch.randn((3, 1, 6, D), device=DEV).to(torch.bfloat16)
+    slots = torch.tensor([5, 17, 40, 41, 100, 200], device=DEV).view(3, 1, 2)
+    where = torch.arange(3, dtype=I32, device=DEV)
+    for x, at in ((near, slots), (far, slots + shift * P)):
+        kvc.kvc_norm_rope_write(x, qkv, where, at, torch.zeros((3, 1, 2, D), dtype=torch.bfloat16, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(big[shift:], c.k_pool)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_queries_and_outputs_at_odd_addresses(dtype):
+    """Contiguous arrays that begin anywhere in an allocation."""
+    c, _ = cache_of([300, 77, 9, 1000], 16, 64, dtype, 2, 1, 2, seed=12, device=DEV)
+    q = torch.randn((2, 1, 6, 64), device=DEV).to(DT[dtype])
+    odd = torch.zeros(q.numel() + 1, dtype=DT[dtype], device=DEV)[1:].view(q.shape)
+    odd.copy_(q)
+    qp = torch.full((2,), 2**31 - 1, dtype=I32, device=DEV)
+    want = check_attention(c, q, qp)
+    pos = torch.zeros(c.slot_pos.numel() + 1, dtype=I32, device=DEV)[1:].view(c.slot_pos.shape)
+    pos.copy_(c.slot_pos)
+    moved = kvc.Cache(c.k_pool, c.v_pool, c.block_table, c.row_len, pos, None, 2, 1, 2)
+    out = torch.zeros(q.numel() + 1, device=DEV)[1:].view(q.shape)
+    lse = torch.zeros(13, device=DEV)[1:].view(2, 1, 6)
+    st = status()
+    kvc.kvc_block_attention(moved, odd, qp, out, lse, words(kvc.kvc_block_attention_workspace_bytes(4, 3, 64)), None, None, st)
+    assert code(st) == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    mp = c.block_table.shape[1]
+    b, bp = torch.randn((4, mp, 2, 64), device=DEV).to(DT[dtype]).sort(2)[0].contiguous(), torch.zeros((4, mp), dtype=I32, device=DEV)
+    one, other = select(c, b, bp, q, qp, 7), select(moved, b, bp, odd, qp, 7)
+    assert torch.equal(one[0], other[0]) and torch.equal(one[1], other[1])
+
+
+def test_select_scores_that_32_bits_cannot_tell_apart():
+    """Pages whose scores differ by less than fp32 resolves, in every order: the choice is that of 64 bits."""
+    D, P, n = 128, 16, 600
+    c, _ = cache_of([n * P], P, D, "f32", 1, 1, 1, seed=13, device=DEV, late=False)
+    mp = c.block_table.shape[1]
+    g = torch.Generator(device=DEV).manual_seed(3)
+    base = torch.randn((D,), device=DEV, generator=g)
+    lo = base.repeat(1, mp, 1).clone()
+    where = torch.randint(0, D, (mp,), device=DEV, generator=g)
+    ulps = torch.randint(-3, 4, (mp,), device=DEV, generator=g)
+    for b in range(mp):
+        lo[0, b, where[b]] *= 1 + int(ulps[b]) * 2.0**-23
+    bounds = torch.stack((lo, lo + 1), 2).contiguous()
+    q = torch.randn((1, 1, 3, D), device=DEV, generator=g)
+    pos, qp = torch.zeros((1, mp), dtype=I32, device=DEV), torch.zeros(1, dtype=I32, device=DEV)
+    for k in (1, 17, 300, 599):
+        check_select(c, bounds, pos, q, qp, k)
+    big = bounds * 1e37  # sums past fp32's range: nothing is known in 32 bits
+    for k in (1, 17, 300):
+        check_select(c, big, pos, 1e3 * q, qp, k)
