@@ -316,9 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < kRing - 1; ++i) ok[i] = issue(i, i);
 
-    // while the first chunks come: rows without slots, a thread a row to look and a warp a row to write
-    for (int r0 = blockIdx.x * kThreads + warp * 32; r0 < c.rows; r0 += gridDim.x * kThreads) {
-        unsigned empty = __ballot_sync(0xffffffffu, r0 + lane < c.rows && row_slots(a, r0 + lane, false) == 0);
+    // while the first chunks come: rows without slots, an even share of the rows a warp, a lane a row to look
+    const int rows_each = (c.rows + (int)gridDim.x * kWarps - 1) / ((int)gridDim.x * kWarps);
+    const int e0 = (warp * (int)gridDim.x + (int)blockIdx.x) * rows_each, e1 = min(c.rows, e0 + rows_each);
+    for (int r0 = e0; r0 < e1; r0 += 32) {
+        unsigned empty = __ballot_sync(0xffffffffu, r0 + lane < e1 && row_slots(a, r0 + lane, false) == 0);
         for (; empty; empty &= empty - 1) {
             const int r = r0 + __ffs(empty) - 1;
             const int64_t head = (int64_t)(r / Hkv) * a.num_q_heads + (r % Hkv) * G;
