@@ -39,7 +39,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMinRun = 2;     // chunks a run, where there are that many
+constexpr int kMinRun = 1;     // chunks a run (2: 11.3 us where 1 takes 10.0 for 8 rows of 512 slots, and no faster at other sizes)
 constexpr int kMaxGroup = 8;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kJoinThreads = 256;

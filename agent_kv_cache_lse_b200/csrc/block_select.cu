@@ -152,20 +152,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_score_kernel(SelectArgs
     if (b0 < nb) load(b0);
     factors<T, D>(a, row, w);
     __syncthreads();
-    if (blockIdx.x == 0) {  // U, summed in 64 bits and rounded up
-        double x = 0;
-        for (int d = threadIdx.x; d < D; d += kThreads) x += w[D + d] - w[d];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) red[threadIdx.x >> 5] = __double2float_ru(x);
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            float all = 0.f;
-            for (int i = 0; i < kWarps; ++i) all = __fadd_ru(all, red[i]);
-            a.stats[(int64_t)row * (1 + a.spread)] = all;
-        }
-        __syncthreads();
-    }
     constexpr int E = Element<T>::N;
     float2 wr[LOADS][N / E];  // the factors of a word's elements
 #pragma unroll
@@ -224,6 +210,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_score_kernel(SelectArgs
     if (threadIdx.x == 0) {
         for (int i = 1; i < kWarps; ++i) top = fmaxf(top, red[i]);
         a.stats[(int64_t)row * (1 + a.spread) + 1 + blockIdx.x] = top;
+    }
+    if (blockIdx.x == 0) {  // U, summed in 64 bits and rounded up
+        double x = 0;
+        for (int d = threadIdx.x; d < D; d += kThreads) x += w[D + d] - w[d];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        __syncthreads();  // red is read
+        if (lane == 0) red[threadIdx.x >> 5] = __double2float_ru(x);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            float all = 0.f;
+            for (int i = 0; i < kWarps; ++i) all = __fadd_ru(all, red[i]);
+            a.stats[(int64_t)row * (1 + a.spread)] = all;
+        }
     }
 }
 

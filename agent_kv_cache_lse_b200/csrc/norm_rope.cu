@@ -133,6 +133,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(NormRopeArgs
     const bool in = p0 * N < R;
     const int64_t pool_slots = c.num_pages * c.page_size;
 
+    // this lane's frequencies, for the pairs it makes of each token
+    float freq[kMaxD / 64];
+#pragma unroll
+    for (int i = 0; i < kMaxD / 64; ++i) freq[i] = lane + 32 * i < half ? a.inv_freq[lane + 32 * i] : 0.f;
+
     // the run
     const int tokens = a.token_count ? min(max(*a.token_count, 0), a.num_tokens) : a.num_tokens;
     const int64_t all = (int64_t)tokens * L * (sq + skv), W = min((int64_t)gridDim.x * kWarps, all);
@@ -228,7 +233,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) norm_rope_kernel(NormRopeArgs
         if ((t != token || made != 2 * l + kv) && !(kv && h0 >= Hkv)) {  // values alone need no factors
             if (t != token && half) {
                 const int pos = *reinterpret_cast<const int32_t *>(stage + kVectors + 256);
-                for (int j = lane; j < half; j += 32) cs[j] = turn(pos, a.inv_freq[j]);
+#pragma unroll
+                for (int i = 0; i < kMaxD / 64; ++i)
+                    if (lane + 32 * i < half) cs[lane + 32 * i] = turn(pos, freq[i]);
                 __syncwarp();
             }
             token = t;
