@@ -39,6 +39,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+static_assert(kThreads == kShareThreads, "rows are shared out by the whole CTA");
 constexpr int kMinRun = 1;     // chunks a run (2: 11.3 us where 1 takes 10.0 for 8 rows of 512 slots, and no faster at other sizes)
 constexpr int kMaxGroup = 8;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     constexpr int LK = D / 8, KW = 32 / LK, STEPS = CH / KW;  // fp32: lanes a key, keys a step
     constexpr float kSlack = 8.f;                     // bf16: the maximum moves only when a logit passes it by 8 (log2)
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ RunTable<kWarps> runs;
+    __shared__ RunTable runs;
     __shared__ int4 segs[2 * kWarps];  // parts left in shared memory, in order: row (-1: none), begins here, ends here,
                                        // chunks the row has after the run
     const CacheView &c = a.c;
@@ -161,18 +162,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     begin_dependent();
     if (tid < 2 * kWarps) segs[tid] = make_int4(-1, 0, 0, 0);
     if (tid == 0) a.spans[blockIdx.x] = make_int2(-1, 0);
+    int w, crow, coff;  // this warp's run; the next chunk to look up
     const Share sh = share_rows<kWarps>(c.rows, kMinRun, runs, [&](int r) {
         return (row_slots(a, r, blockIdx.x == 0) + CH - 1) / CH;
-    });
+    }, w, crow, coff);
     unsigned char *ring = smem + (size_t)warp * kRing * kStage;
     const T *kp = static_cast<const T *>(c.k_pool);
     const T *vp = static_cast<const T *>(c.v_pool);
     // where a run's first part goes when its row ends in the run but began before it; its last part goes to the warp's
     // own ring, which is free by then
     float *head_part = reinterpret_cast<float *>(smem + (size_t)kWarps * kRing * kStage) + warp * rec;
-    const int w = blockIdx.x * sh.per_cta + warp;
-    const bool works = warp < sh.per_cta && w < sh.W;
-    int total = works ? (int)(run_start(sh, w + 1) - run_start(sh, w)) : 0;  // chunks of the run
+    int total = w < sh.W ? (int)(run_start(sh, w + 1) - run_start(sh, w)) : 0;  // chunks of the run
 
     // Lookups.  Lane l of batch j knows chunk 32 j + l of the run: its row, its place in the row's chunks and how many follow
     // it there, and, where a chunk lies in one page (kWhole: the page size is a multiple of CH), its first slot (-1: not
@@ -180,7 +180,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a) {
     // loads go on across rows.  Else every lane looks up the page of its own key, one chunk ahead.
     int b_row[2], b_off[2], b_left[2], b_slot[2], b_keys[2];
     int64_t b_src[2];
-    int crow = works ? runs.row[warp] : 0, coff = works ? runs.off[warp] : 0;  // the next chunk to look up
     int cslots = total > 0 ? row_slots(a, crow, false) : 0;
     auto look = [&](int row, int stream, int slots, int &slot, int64_t &src, int &keys) {
         slot = -1;

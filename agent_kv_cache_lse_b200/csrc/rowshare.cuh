@@ -37,27 +37,24 @@ __device__ __forceinline__ Share share_units(int64_t U, int ctas, int min_run) {
     return s;
 }
 
-template <int kRuns>
+constexpr int kShareThreads = 256;  // threads of a CTA that shares rows
+
 struct RunTable {
-    long long scan[32];
-    int row[kRuns];     // the run's first row ...
-    int off[kRuns];     // ... and its first unit in that row
+    long long scan[kShareThreads / 32];
+    long long before[kShareThreads];  // units before each thread's rows
 };
 
-// Share out the rows' units, count(r) of them in row r.  Every CTA sums the counts itself (each thread its share of
-// the rows, then a scan over the CTA) and finds where its runs start.  All threads call it; the table is ready on return.
+// Share out the rows' units, count(r) of them in row r.  Every CTA sums the counts itself: each thread its share of
+// the rows, then a scan over the CTA.  Warp k of a CTA takes the CTA's k-th run, if it has one (`run` below W): it finds the
+// run's first row, and its first unit in that row, in the scan.  All threads of the CTA call it, whole warps with the same
+// results; row and off are 0 for a warp without a run.
 template <int kRuns, typename Count>
-__device__ __forceinline__ Share share_rows(int rows, int min_run, RunTable<kRuns> &t, Count count) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    const int each = (rows + (int)blockDim.x - 1) / (int)blockDim.x;
+__device__ __forceinline__ Share share_rows(int rows, int min_run, RunTable &t, Count count, int &run, int &row, int &off) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (rows + kShareThreads - 1) / kShareThreads;
     const int r0 = min(rows, tid * each), r1 = min(rows, r0 + each);
     long long mine = 0;
-    int first = 0;
-    for (int r = r0; r < r1; ++r) {
-        const int n = count(r);
-        if (r == r0) first = n;
-        mine += n;
-    }
+    for (int r = r0; r < r1; ++r) mine += count(r);
     long long x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -68,28 +65,44 @@ __device__ __forceinline__ Share share_rows(int rows, int min_run, RunTable<kRun
     __syncthreads();
     long long before = x - mine;
     int64_t U = 0;
-    for (int k = 0; k < nw; ++k) {
+#pragma unroll
+    for (int k = 0; k < kShareThreads / 32; ++k) {
         if (k < warp) before += t.scan[k];
         U += t.scan[k];
     }
-    const Share s = share_units<kRuns>(U, gridDim.x, min_run);
-    if (mine > 0) {
-        // the CTA's runs that start in this thread's rows
-        const int w0 = blockIdx.x * s.per_cta;
-        for (int k = 0; k < s.per_cta && w0 + k < s.W; ++k) {
-            const int64_t at = run_start(s, w0 + k);
-            if (at < before || at >= before + mine) continue;
-            int64_t left = at - before;
-            int r = r0, n = first;
-            while (left >= n) {
-                left -= n;
-                n = count(++r);
-            }
-            t.row[k] = r;
-            t.off[k] = (int)left;
-        }
-    }
+    t.before[tid] = before;
     __syncthreads();
+    const Share s = share_units<kRuns>(U, gridDim.x, min_run);
+    run = warp < s.per_cta ? (int)blockIdx.x * s.per_cta + warp : s.W;
+    row = off = 0;
+    if (run >= s.W) return s;
+    // the thread whose rows hold the run's first unit: the last with no more units before it
+    const int64_t at = run_start(s, run);
+    int who = 0;
+#pragma unroll
+    for (int step = kShareThreads / 2; step > 0; step /= 2)
+        if (t.before[who + step] <= at) who += step;
+    int left = (int)(at - t.before[who]);
+    row = who * each;
+    for (int end = min(rows, row + each); row < end; row += 32) {  // of its rows, 32 at a time
+        const int n = row + lane < end ? count(row + lane) : 0;
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, incl > left);
+        if (past) {
+            const int k = __ffs(past) - 1;
+            off = left - __shfl_sync(0xffffffffu, incl - n, k);
+            row += k;
+            return s;
+        }
+        left -= __shfl_sync(0xffffffffu, incl, 31);
+    }
+    run = s.W;  // only if the counts changed meanwhile
+    row = 0;
     return s;
 }
 
