@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kFillThreads = 256;
+constexpr int kBatch = 4;          // rows whose loads a planning thread has side by side
 constexpr int kTile = 32;          // tokens a CTA of the fill takes
 constexpr int kStarts = 1024;      // sequences whose token_start a CTA searches in shared memory
 constexpr int kAloneTiles = 4;     // tiles (kTile tokens of 32 rows) that the planning CTA fills itself
@@ -62,21 +63,6 @@ __device__ __forceinline__ int count_of(const ReserveArgs &a, int s) { return ma
 // positions next_pos .. next_pos + c - 1 must be token positions (0 .. INT32_MAX - 1)
 __device__ __forceinline__ bool bad_positions(const ReserveArgs &a, int s, int cnt) {
     return cnt > 0 && (a.next_pos[s] < 0 || (int64_t)a.next_pos[s] + cnt > INT32_MAX);
-}
-
-// new pages of row r, or -1 and the device code when the row cannot take its tokens
-__device__ __forceinline__ int row_need(const ReserveArgs &a, int r, int *code) {
-    const CacheView &c = a.c;
-    const int s = r / (c.num_layers * c.num_kv_heads), n = a.c.row_len[r], cnt = count_of(a, s);
-    if (cnt == 0) return 0;
-    if (n < 0 || n > c.max_slots || bad_positions(a, s, cnt)) return *code = KVC_DEV_BAD_LENGTH, -1;
-    if ((int64_t)n + cnt > c.max_slots) return *code = KVC_DEV_FREED_OVERFLOW, -1;
-    const int held = pages_for(a, n);
-    if (held * c.page_size != n) {  // the first token joins the row's last page
-        const int32_t pg = c.block_table[(int64_t)r * c.max_pages_per_row + held - 1];
-        if (pg < 0 || pg >= c.num_pages) return *code = KVC_DEV_BAD_PAGE, -1;
-    }
-    return pages_for(a, n + cnt) - held;
 }
 
 // the sequence of token t: token_start[s] <= t < token_start[s + 1]
@@ -182,12 +168,43 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_plan_kernel(ReserveAr
         if (a.new_count[s] < 0) report(a.status, KVC_DEV_BAD_LENGTH, s * per);
         tokens += count_of(a, s);
     }
-    for (int r = r0; r < r1; ++r) {
-        int code = 0;
-        const int need = row_need(a, r, &code);
-        if (need < 0) report(a.status, code, r);
-        a.ws[r] = need < 0 ? -1 : pages;
-        pages += max(need, 0);
+    // the new pages of each row (-1: it cannot take its tokens), kBatch rows with their loads side by side
+    int len[kBatch], cnt[kBatch];
+    int64_t off[kBatch];  // the row's first new page among this thread's (-1: refused); one batch is kept to the end, more go through ws
+    for (int b0 = r0; b0 < r1; b0 += kBatch) {
+        int next[kBatch], code[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = b0 + k, s = r < r1 ? r / per : 0;
+            len[k] = r < r1 ? c.row_len[r] : 0;
+            cnt[k] = r < r1 ? count_of(a, s) : 0;
+            next[k] = r < r1 ? a.next_pos[s] : 0;
+        }
+        int32_t joined[kBatch];  // the page that a row's first token joins
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            code[k] = KVC_DEV_OK;
+            joined[k] = 0;
+            if (cnt[k] == 0) continue;
+            if (len[k] < 0 || len[k] > c.max_slots || next[k] < 0 || (int64_t)next[k] + cnt[k] > INT32_MAX) {
+                code[k] = KVC_DEV_BAD_LENGTH;
+            } else if ((int64_t)len[k] + cnt[k] > c.max_slots) {
+                code[k] = KVC_DEV_FREED_OVERFLOW;
+            } else {
+                const int held = pages_for(a, len[k]);
+                if (held * c.page_size != len[k]) joined[k] = c.block_table[(int64_t)(b0 + k) * c.max_pages_per_row + held - 1];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = b0 + k;
+            if (r >= r1) continue;
+            if (code[k] == KVC_DEV_OK && (joined[k] < 0 || joined[k] >= c.num_pages)) code[k] = KVC_DEV_BAD_PAGE;
+            if (code[k] != KVC_DEV_OK) report(a.status, code[k], r);
+            off[k] = code[k] == KVC_DEV_OK ? pages : -1;
+            if (r1 - r0 > kBatch) a.ws[r] = off[k];
+            if (code[k] == KVC_DEV_OK && cnt[k]) pages += pages_for(a, len[k] + cnt[k]) - pages_for(a, len[k]);
+        }
     }
     long long xt = tokens, xp = pages;
 #pragma unroll
@@ -220,11 +237,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_plan_kernel(ReserveAr
         *a.free_count_out = refuse ? depth : depth - all_pages;
     }
     const long long base = depth - all_pages + (w ? before_p : 0) + xp - pages;
-    for (int r = r0; r < r1; ++r) {
-        const bool take = !refuse && a.ws[r] >= 0;
-        if (take) a.ws[r] += base;
-        const int n = c.row_len[r];
-        a.row_len_out[r] = take ? n + count_of(a, r / per) : n;
+    for (int b0 = r0; b0 < r1; b0 += kBatch) {
+        if (r1 - r0 > kBatch) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (b0 + k < r1) off[k] = a.ws[b0 + k], len[k] = c.row_len[b0 + k], cnt[k] = count_of(a, (b0 + k) / per);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (b0 + k < r1) {
+                const bool take = !refuse && off[k] >= 0;
+                a.ws[b0 + k] = take ? base + off[k] : -1;
+                a.row_len_out[b0 + k] = take ? len[k] + cnt[k] : len[k];
+            }
     }
     if constexpr (kAlone) {
         __syncthreads();  // what the CTA wrote above is read below

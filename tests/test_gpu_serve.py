@@ -105,6 +105,9 @@ def test_reserve_in_place_many_rows_without_optional_arrays():
     counts = rng.integers(0, 4, 1100).tolist()
     assert reserve_case(lengths, counts, 16, 1100, 1, 2, 6, optional=False, in_place=True)[0] == 0
     assert reserve_case(lengths[:8], [700, 0, 1, 2000], 16, 4, 1, 2, 7, in_place=True)[0] == 0
+    lengths = rng.integers(0, 40, 2500 * 2).tolist()  # more than four rows a planning thread
+    got, want = reserve_case(lengths, rng.integers(0, 4, 2500).tolist(), 16, 2500, 1, 2, 9, in_place=True)
+    assert got == 0 and not want["refused"]
 
 
 def test_reserve_exact_stack_and_tokens():
