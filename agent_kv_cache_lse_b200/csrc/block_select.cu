@@ -24,7 +24,7 @@
 //   digit in which the k-th key lies, usually with a handful of keys, which are ranked directly; while there are more than
 //   kFew, the next 11 bits follow.  The 64-bit scores between c - 2 e and c + 2 e, if they have to be ranked, go the same
 //   way.  One pass in index order then lists the pages.
-// Measured: 78 us for 677,000 pages of 512 rows (16 sequences of 8K to 33K tokens, 4 layers; 62 us launch A, 5.6 TB/s), 89 us with
+// Measured: 77 us for 677,000 pages of 512 rows (16 sequences of 8K to 33K tokens, 4 layers; 62 us launch A, 5.6 TB/s), 89 us with
 // 64-bit scores throughout; 11 us for 8 rows of 2,048 pages, of which the bytes are 1.3 (a dozen barriers of launch B the rest).
 #include <cuda_bf16.h>
 
@@ -42,6 +42,7 @@ constexpr int kCtas = 8;           // of the scoring launch, a multiprocessor
 constexpr int kPages = 4;          // loads a lane has in flight
 constexpr int kPickThreads = 512;
 constexpr int kBins = 2048, kBits = 11;
+constexpr int kAhead = 4;          // keys a picking thread has in flight beside the row's length
 constexpr int kFew = 32;           // keys that one warp ranks
 constexpr int kCached = 16384;     // keys of a row that stay in shared memory
 
@@ -335,11 +336,18 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
     begin_dependent();
     const CacheView &c = a.c;
     const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, P = c.page_size;
+    const int64_t base = (int64_t)row * c.max_pages_per_row;
+    const uint32_t *keys = a.keys + base;
+    // the first keys of a thread come with the row's length (past it they are whatever the workspace held, and not used)
+    uint32_t ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int b = tid + i * kPickThreads;
+        ahead[i] = b < c.max_pages_per_row ? keys[b] : 0;
+    }
     int n = c.row_len[row];
     if (n < 0 || n > c.max_slots) n = 0;
     const int nb = (n + P - 1) / P;
-    const int64_t base = (int64_t)row * c.max_pages_per_row;
-    const uint32_t *keys = a.keys + base;
     const float *stats = a.stats + (int64_t)row * (1 + a.spread);
     int32_t *list = a.block_list + (int64_t)row * a.top_k;
     // what there is: pages that can be taken, that always are, the range of the others' keys, the largest bound
@@ -348,8 +356,7 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
     float top = 0.f;
     for (int i = tid; i < min(a.ctas, (nb + a.pages_a_cta - 1) / a.pages_a_cta); i += kPickThreads) top = fmaxf(top, stats[1 + i]);
     const float U = nb > 0 ? stats[0] : 0.f;
-    for (int b = tid; b < nb; b += kPickThreads) {
-        const uint32_t key = keys[b];
+    auto count = [&](int b, uint32_t key) {
         if (nb <= kCached) cache[b] = key;
         visible += key != 0;
         if (key == kAlways) {
@@ -358,7 +365,11 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
             lo = min(lo, key);
             hi = max(hi, key);
         }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (tid + i * kPickThreads < nb) count(tid + i * kPickThreads, ahead[i]);
+    for (int b = tid + kAhead * kPickThreads; b < nb; b += kPickThreads) count(b, keys[b]);
     if (nb <= kCached) keys = cache;
     visible = __reduce_add_sync(0xffffffffu, visible);
     always = __reduce_add_sync(0xffffffffu, always);
