@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_plan_kernel(ReserveAr
         a.token_start[s] = (int)min(at, (long long)a.max_tokens);
         at += count_of(a, s);
     }
-    const bool over = all_tokens > a.max_tokens, shallow = depth > a.free_capacity || (all_pages > 0 && all_pages > depth), refuse = over || shallow;
+    const bool over = all_tokens > a.max_tokens, shallow = depth < 0 || depth > a.free_capacity || all_pages > depth;
+    const bool refuse = over || shallow;
     // the depth was read by everyone before the barrier above, so free_count_out may be free_count
     if (tid == 0) {
         if (refuse) report(a.status, over ? KVC_DEV_BAD_LENGTH : KVC_DEV_FREED_OVERFLOW, -1);

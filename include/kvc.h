@@ -357,7 +357,7 @@ size_t kvc_reserve_workspace_bytes(int32_t rows);
  * In/out: the cache's block_table (entries of new pages), slot_pos and slot_label (`label`), and crf
  *       ([rows][max_slots] fp32, may be NULL; 0) of the new slots.  k_pool and v_pool are not touched.
  * Device faults: more than max_tokens tokens (KVC_DEV_BAD_LENGTH, row -1), or a stack too shallow or
- * deeper than free_capacity (KVC_DEV_FREED_OVERFLOW, row -1), reserve nothing: row_len_out and free_count_out get the old values and the slot
+ * a depth outside [0, free_capacity] (KVC_DEV_FREED_OVERFLOW, row -1), reserve nothing: row_len_out and free_count_out get the old values and the slot
  * map -1 throughout.  A row is left alone and its slots are -1 when it would exceed max_slots
  * (KVC_DEV_FREED_OVERFLOW), its length is out of range or its positions would leave [0, INT32_MAX)
  * (KVC_DEV_BAD_LENGTH), or the page its first new token joins is bad (KVC_DEV_BAD_PAGE).  A negative count is

@@ -34,7 +34,7 @@ def reserve_slots(bt, row_len, slot_pos, slot_label, crf, new_count, next_pos, l
         else:
             takes[r] = -(-(n + c) // P) - -(-n // P)
     total = sum(takes.values())
-    if start[-1] > max_tokens or depth > len(free_pages) or (total > 0 and total > depth):
+    if start[-1] > max_tokens or not 0 <= depth <= len(free_pages) or total > depth:
         refused[-1] = "call"
         return out
     for s in range(S):

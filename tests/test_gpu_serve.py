@@ -115,6 +115,8 @@ def test_reserve_exact_stack_and_tokens():
     assert reserve_case(lengths, counts, 16, 2, 1, 2, 8, spare=0, max_tokens=23)[0] == 0
     got, want = reserve_case(lengths, counts, 16, 2, 1, 2, 8, deeper=1)  # a depth past the end of the stack's array
     assert got == 5 and -1 in want["refused"]
+    got, want = reserve_case([5, 6], [1], 16, 1, 1, 2, 8, spare=0, deeper=-1)  # below none, though no page is needed
+    assert got == 5 and -1 in want["refused"]
     got, want = reserve_case(lengths, counts, 16, 2, 1, 2, 8, spare=-1)
     assert got == 5 and -1 in want["refused"]
     got, want = reserve_case(lengths, counts, 16, 2, 1, 2, 8, max_tokens=22)
