@@ -11,9 +11,10 @@
 // 64-bit arithmetic for every page took 80 instructions a page and warp and 1.4 times the time of the bytes.  But only pages
 // at the border need it.  With x in 32 bits, of 8 multiply-adds a lane and 5 sums across lanes on factors rounded once (14
 // roundings of at most 2^-24 each, of sums of magnitudes), |x - score| <= e = 2^-20 M U, where M bounds |lo| and |hi| over the row and
-// U = sum_d up_d - down_d.  If c is the k-th largest x, a page above c + 2 e has a score above those of all but fewer than
-// k pages and is taken, one below c - 2 e is not, and the pages between are ranked by their scores in 64 bits: mostly there is one
-// page between, and nothing to rank.
+// U = sum_d up_d - down_d, as long as no sum can leave fp32's range (M U < 2^126; past it every page is ranked in 64 bits).
+// If c is the k-th largest x, a page above c + 2 e has a score above those of all but fewer than k pages and is taken, one
+// below c - 2 e is not, and the pages between are ranked by their scores in 64 bits: mostly there is one page between, and
+// nothing to rank.
 //
 // Launch A: a warp takes kPages loads' pages at a time, 16 bytes a lane of [lo | hi], the matching up or down in registers.
 //   The pages' sums are joined together, halving the pages a lane holds with each of the first two shuffles.  x becomes an
@@ -410,10 +411,11 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
             key = keys[b];
             return key != 0 && key != kAlways;
         }).cut);
-        const float e = 2.1f * (0x1p-20f * top * U + 0x1p-130f);  // 2 e, with room for the roundings here
+        const float reach = top * U;  // no partial sum of a finite page is larger
+        const float e = 2.1f * (0x1p-20f * reach + 0x1p-130f);  // 2 e, with room for the roundings here
         from = 1;
         above = kAlways - 1;
-        if (e < 1e37f) {  // else nothing is known
+        if (reach < 0x1p126f) {  // else a sum may have left fp32's range (inf, or NaN from two signs), and nothing is known
             from = float_key(x - e);
             above = float_key(x + e);
         }

@@ -590,3 +590,37 @@ def test_select_scores_that_32_bits_cannot_tell_apart():
     big = bounds * 1e37  # sums past fp32's range: nothing is known in 32 bits
     for k in (1, 17, 300):
         check_select(c, big, pos, 1e3 * q, qp, k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("reach", [1e36, 1e38, 1e39, 1e40, 1e42, 1e44])
+def test_select_sums_that_leave_fp32(dtype, D, reach):
+    """Unlike pages whose sums of magnitudes come to `reach`: single sums past fp32's range of either sign, and sums in range
+    of terms that are not.  The choice is that of 64 bits all the same."""
+    n = 400
+    c, _ = cache_of([n * 16, n * 16], 16, D, dtype, 2, 1, 1, seed=14, device=DEV, late=False)
+    mp = c.block_table.shape[1]
+    g = torch.Generator(device=DEV).manual_seed(D)
+    size = 10 ** (4 * torch.rand((2, mp, 1, 1), device=DEV, generator=g, dtype=torch.float64) - 4)
+    b = torch.randn((2, mp, 2, D), device=DEV, generator=g, dtype=torch.float64).clamp(-3, 3).sort(2)[0]
+    q = torch.randn((2, 1, 2, D), device=DEV, generator=g, dtype=torch.float64)
+    unit = reach ** 0.5 / D ** 0.5  # sums of 2 D terms of about unit * unit
+    b, q = (b * size * unit / 3).to(DT[dtype]), (q * unit).to(DT[dtype])
+    pos, qp = torch.zeros((2, mp), dtype=I32, device=DEV), torch.zeros(2, dtype=I32, device=DEV)
+    for k in (2, 5, 100, 200, 300, 399):
+        check_select(c, b.contiguous(), pos, q, qp, k, 1, 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_select_one_page_past_fp32_among_ordinary_ones(dtype):
+    """Lanes of one page overflow with both signs; its score is far below the others'."""
+    c, _ = cache_of([40 * 16], 16, 64, dtype, 1, 1, 1, seed=15, device=DEV, late=False)
+    mp = c.block_table.shape[1]
+    b = torch.ones((1, mp, 2, 64), device=DEV)
+    b[:, :, 0] = -1
+    b[0, 17, 1, 0:4], b[0, 17, 1, 4:8], b[0, 17, 0] = 3e37, -3.1e37, -3.2e37
+    q = torch.full((1, 1, 1, 64), 1e3, device=DEV)
+    pos, qp = torch.zeros((1, mp), dtype=I32, device=DEV), torch.zeros(1, dtype=I32, device=DEV)
+    for k in (1, 7, 39):
+        check_select(c, b.to(DT[dtype]), pos, q.to(DT[dtype]), qp, k)
