@@ -442,6 +442,24 @@ def _tables(cache: Cache, rows: int, mp: int, P: int, dev: int):
     _arg(cache.slot_pos, "slot_pos", (rows, mp * P), _I32, dev)
 
 
+def _qkv(qkv: torch.Tensor, L: int, H: int, D: int, dt, dev: int):
+    """(tokens, query heads, elements between tokens) of a step's qkv [T][L][Hq + 2 H][D], whose tokens may lie in a wider array."""
+    if qkv.dim() != 4 or qkv.shape[1] != L or qkv.shape[3] != D or qkv.shape[2] <= 2 * H:
+        raise KvcError(f"qkv: shape {tuple(qkv.shape)}, expected (*, {L}, Hq + {2 * H}, {D})")
+    T, heads = qkv.shape[0], qkv.shape[2]
+    if qkv.dtype is not dt:
+        raise KvcError(f"qkv: dtype {qkv.dtype}, expected {dt}")
+    if qkv.get_device() != dev:
+        raise KvcError(f"qkv: on {qkv.device}, the cache is elsewhere")
+    token = apart = L * heads * D
+    if not qkv.is_contiguous():
+        apart = qkv.stride(0)
+        if not qkv[0].is_contiguous() or (T > 1 and apart < token):
+            raise KvcError("qkv must be contiguous within a token, and tokens may not overlap")
+        apart = max(apart, token)
+    return T, heads - 2 * H, apart
+
+
 def _call(name: str, dev: int, stream, *args):
     """Call entry point `name` with the cache's device current, on `stream` or that device's current stream."""
     if dev < 0:
@@ -501,20 +519,7 @@ def kvc_norm_rope_write(cache: Cache, qkv: torch.Tensor, token_pos: torch.Tensor
         return
     c, _, _, _, D, dt, dev = _cache_args(cache)
     L, H = cache.num_layers, cache.num_kv_heads
-    if qkv.dim() != 4 or qkv.shape[1] != L or qkv.shape[3] != D or qkv.shape[2] <= 2 * H:
-        raise KvcError(f"qkv: shape {tuple(qkv.shape)}, expected (*, {L}, Hq + {2 * H}, {D})")
-    T, heads = qkv.shape[0], qkv.shape[2]
-    Hq, token = heads - 2 * H, L * heads * D
-    if qkv.dtype is not dt:
-        raise KvcError(f"qkv: dtype {qkv.dtype}, expected {dt}")
-    if qkv.get_device() != dev:
-        raise KvcError(f"qkv: on {qkv.device}, the cache is elsewhere")
-    apart = token
-    if not qkv.is_contiguous():
-        apart = qkv.stride(0)
-        if not qkv[0].is_contiguous() or (T > 1 and apart < token):
-            raise KvcError("qkv must be contiguous within a token, and tokens may not overlap")
-        apart = max(apart, token)
+    T, Hq, apart = _qkv(qkv, L, H, D, dt, dev)
     half = 0 if inv_freq is None else inv_freq.shape[0]
     _call("kvc_norm_rope_write", dev, stream, c, qkv.data_ptr(), apart, T,
           _opt(token_count, "token_count", (1,), _I32, dev), Hq, _opt(q_weight, "q_weight", (L, D), dt, dev),

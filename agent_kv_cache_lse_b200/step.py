@@ -10,10 +10,12 @@ matter for it.
 with torch and marshals arguments.  The free-page stack may be the freed list of an ``EvictionRound`` (its ``freed`` and
 ``num_freed``), so that pages go round between eviction and new tokens; after a compaction, which moves entries
 between pages, call ``refresh``.  All calls take device tensors and do not synchronise, so a step can be captured into a
-CUDA graph; two graphs of one ServingStep share its buffers and must not overlap.
+CUDA graph; two graphs of one ServingStep share its buffers and must not overlap.  A call whose arguments are refused
+(kvc.KvcError) is refused before anything is enqueued: the cache and the stack are as they were.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -28,7 +30,10 @@ class ServingStep:
                  inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, crf: Optional[torch.Tensor] = None):
         """max_tokens: the most tokens one call brings; free_pages, free_count: the stack (free_count: one int64);
         q_weight, k_weight [L][D], eps, inv_freq, interleaved: as for kvc_norm_rope_write; crf: the rows' LRFU values, which
-        new slots start at 0."""
+        new slots start at 0.  With a page budget top_k, sink_blocks + recent_blocks may not exceed it."""
+        self._check_sizes(cache, num_q_heads, max_tokens, top_k, sink_blocks, recent_blocks)
+        self._check_factors(cache, q_weight, k_weight, eps, inv_freq)
+        self.num_q_heads = num_q_heads
         self.cache, self.free_pages, self.free_count, self.crf = cache, free_pages, free_count, crf
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, eps
         self.inv_freq, self.interleaved = inv_freq, interleaved
@@ -48,12 +53,55 @@ class ServingStep:
         self.out, self.lse = empty(S, L, num_q_heads, D), empty(S, L, num_q_heads)
         self.status = empty(2, dtype=i32)
         self.reserve_ws = empty(kvc.kvc_reserve_workspace_bytes(rows) // 8, dtype=torch.int64)
-        self.attend_ws = empty(-(-kvc.kvc_block_attention_workspace_bytes(rows, num_q_heads // H, D) // 8), dtype=torch.int64)
+        with torch.cuda.device_of(cache.k_pool):  # that workspace depends on the device
+            need = kvc.kvc_block_attention_workspace_bytes(rows, num_q_heads // H, D)
+        self.attend_ws = empty(-(-need // 8), dtype=torch.int64)
         if top_k:
             self.bounds, self.block_pos = empty(rows, mp, 2, D, dtype=dt), empty(rows, mp, dtype=i32)
             self.block_list, self.block_count = empty(rows, top_k, dtype=i32), empty(rows, dtype=i32)
             self.select_ws = empty(kvc.kvc_select_blocks_workspace_bytes(rows, mp) // 8, dtype=torch.int64)
             self.refresh()
+
+    @staticmethod
+    def _check_sizes(c, num_q_heads, max_tokens, top_k, sink, recent):
+        if num_q_heads <= 0 or num_q_heads % c.num_kv_heads or num_q_heads // c.num_kv_heads > 128:
+            raise kvc.KvcError(f"num_q_heads: {num_q_heads}, expected 1 to 128 for each of the {c.num_kv_heads} KV heads")
+        if max_tokens < 0 or not 0 <= top_k <= 1 << 24:
+            raise kvc.KvcError(f"max_tokens: {max_tokens}, top_k: {top_k}, expected at least 0 (and a top_k of at most 2^24)")
+        if top_k and (sink < 0 or recent < 0 or sink + recent > top_k):
+            raise kvc.KvcError(f"sink_blocks: {sink}, recent_blocks: {recent}, expected at least 0 and at most top_k = {top_k} together")
+
+    @staticmethod
+    def _check_factors(c, q_weight, k_weight, eps, inv_freq):
+        D, dt, dev = c.k_pool.shape[2], c.k_pool.dtype, c.k_pool.get_device()
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                if kvc._arg(w, name, (c.num_layers, D), dt, dev) & 15:
+                    raise kvc.KvcError(f"{name} must be 16-byte aligned")
+                if not (eps >= 0 and math.isfinite(eps)):
+                    raise kvc.KvcError(f"eps: {eps}, expected a finite number of at least 0")
+        if inv_freq is not None:
+            kvc._arg(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32, dev)
+            if inv_freq.numel() % 8 or 2 * inv_freq.numel() > D:
+                raise kvc.KvcError(f"inv_freq: {inv_freq.numel()} entries, expected a multiple of 8 up to {D // 2}")
+
+    def _check_call(self, qkv, new_count, next_pos, label):
+        """Refuse what one of the entry points would refuse after the reservation has been enqueued, or before it."""
+        c, k = self.cache, self.cache.k_pool
+        dev = k.get_device()
+        T, heads, apart = kvc._qkv(qkv, c.num_layers, c.num_kv_heads, k.shape[2], k.dtype, dev)
+        if heads != self.num_q_heads:
+            raise kvc.KvcError(f"qkv: {heads} query heads, expected {self.num_q_heads}")
+        if T > self.token_pos.shape[0]:
+            raise kvc.KvcError(f"qkv: {T} tokens, expected at most max_tokens = {self.token_pos.shape[0]}")
+        if T and (qkv.data_ptr() | apart * qkv.element_size()) & 15:
+            raise kvc.KvcError("qkv and its tokens must be 16-byte aligned")
+        if self.top_k and c.block_table.shape != self.block_pos.shape:
+            raise kvc.KvcError(f"block_table: shape {tuple(c.block_table.shape)}, expected {tuple(self.block_pos.shape)}")
+        kvc._arg(new_count, "new_count", (c.num_seqs,), torch.int32, dev)
+        kvc._arg(next_pos, "next_pos", (c.num_seqs,), torch.int32, dev)
+        if not 0 <= label <= 255:
+            raise kvc.KvcError(f"label: {label}, expected 0 to 255")
 
     def refresh(self, stream=None):
         """Bounds of all pages (after a compaction, or when the cache was filled some other way)."""
@@ -63,6 +111,10 @@ class ServingStep:
     def extend(self, qkv: torch.Tensor, new_count: torch.Tensor, next_pos: torch.Tensor, label: int = 0, stream=None):
         """new_count[s] tokens of each sequence, packed in qkv [T][L][Hq + 2 Hkv][D] (T at most max_tokens; rows past
         the last token are not read), the first at position next_pos[s].  Their queries are then in self.q."""
+        self._check_call(qkv, new_count, next_pos, label)
+        self._extend(qkv, new_count, next_pos, label, stream)
+
+    def _extend(self, qkv, new_count, next_pos, label, stream):
         c, T = self.cache, qkv.shape[0]
         main = stream if stream is not None else torch.cuda.current_stream(c.k_pool.device)
         with torch.cuda.stream(main):
@@ -77,10 +129,17 @@ class ServingStep:
 
     def decode(self, qkv: torch.Tensor, next_pos: torch.Tensor, label: int = 0, stream=None):
         """One token of each sequence (qkv [S][L][Hq + 2 Hkv][D]) at position next_pos[s], and its attention over the
-        top_k pages of each row, the token's own among them: (out [S][L][Hq][D], lse [S][L][Hq])."""
+        top_k pages of each row, the token's own among them (recent_blocks of at least 1): (out [S][L][Hq][D], lse
+        [S][L][Hq]).  At most 8 query heads for each KV head."""
         c, S = self.cache, self.cache.num_seqs
+        self._check_sizes(c, self.num_q_heads, self.token_pos.shape[0], self.top_k, self.sink_blocks, self.recent_blocks)
+        if self.num_q_heads > 8 * c.num_kv_heads:
+            raise kvc.KvcError("decode: at most 8 query heads per KV head")
+        self._check_call(qkv, self.ones, next_pos, label)
+        if qkv.shape[0] < S:
+            raise kvc.KvcError(f"qkv: {qkv.shape[0]} tokens, expected one for each of {S} sequences")
         main = stream if stream is not None else torch.cuda.current_stream(c.k_pool.device)
-        self.extend(qkv, self.ones, next_pos, label, main)
+        self._extend(qkv, self.ones, next_pos, label, main)
         q, pages = self.q[:S], None
         if self.top_k:
             kvc.kvc_select_blocks(c, self.bounds, self.block_pos, q, next_pos, self.block_list, self.block_count,

@@ -194,3 +194,27 @@ def test_calls_the_native_module_hands_back():
         kvc.kvc_block_attention(c, big, qp, torch.zeros_like(big), torch.zeros((1, 1, 9), device=DEV), ws)
     kvc.kvc_block_attention(c, q, qp, out, lse, ws, stream=torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
+
+
+def test_a_refused_call_changes_nothing():
+    """The step refuses before it reserves: lengths, tables and the stack stay, and the call made right gives what it would have."""
+    c, free = cache_of([100, 31, 64, 7], 16, 64, "bf16", 2, 1, 2, seed=2, spare=40, extra_pages=6, device=DEV)
+    count, next_pos = torch.tensor([len(free)], device=DEV), torch.tensor([100, 64], dtype=I32, device=DEV)
+    st = step.ServingStep(c, 4, 4, free.to(DEV), count, top_k=4, inv_freq=inv_freq(64))
+    x = torch.randn((4, 1, 8, 64), device=DEV).to(torch.bfloat16)
+    ones = torch.ones(2, dtype=I32, device=DEV)
+    before = [t.clone() for t in (c.row_len, c.block_table, c.slot_pos, c.k_pool, c.v_pool, count)]
+    big = torch.randn((5, 1, 8, 64), device=DEV).to(torch.bfloat16)
+    for bad in (big, x.float(), x[:, :, :7], x[..., ::2], x.cpu()):
+        with pytest.raises(kvc.KvcError):
+            st.extend(bad, ones, next_pos)
+        with pytest.raises(kvc.KvcError):
+            st.decode(bad, next_pos)
+    with pytest.raises(kvc.KvcError):
+        st.decode(x[:1], next_pos)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, (c.row_len, c.block_table, c.slot_pos, c.k_pool, c.v_pool, count)))
+    assert st.device_status()[0] == 0
+    st.decode(x, next_pos)
+    torch.cuda.synchronize()
+    assert st.device_status()[0] == 0 and c.row_len.tolist() == [101, 32, 65, 8]
