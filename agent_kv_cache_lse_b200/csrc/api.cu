@@ -361,6 +361,21 @@ kvc_status kvc_step_scores(const kvc_cache *cache, const float *scores, const in
                        "kvc_step_scores launch");
 }
 
+kvc_status kvc_push_pages(int32_t *free_pages, int64_t free_capacity, int64_t *free_count, const int32_t *freed,
+                          int64_t freed_capacity, int64_t *num_freed, int32_t *d_status, kvc_stream_t stream) {
+    g_err[0] = 0;
+    if (free_capacity < 0 || freed_capacity < 0)
+        return fail(KVC_ERR_INVALID_ARGUMENT, "free_capacity and freed_capacity must be >= 0");
+    if (!free_count || !num_freed || (free_capacity > 0 && !free_pages) || (freed_capacity > 0 && !freed))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "free_pages, free_count, freed and num_freed are required");
+    const uintptr_t s = (uintptr_t)free_pages, f = (uintptr_t)freed;
+    if (free_count == num_freed || (s < f + 4 * (uint64_t)freed_capacity && f < s + 4 * (uint64_t)free_capacity))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "the stack and the freed list may not overlap");
+    return cuda_status(kvc::launch_push(free_pages, free_capacity, free_count, freed, freed_capacity, num_freed, d_status,
+                                        (cudaStream_t)stream),
+                       "kvc_push_pages launch");
+}
+
 size_t kvc_reserve_workspace_bytes(int32_t rows) { return rows < 0 ? 0 : ((size_t)rows + 1) * sizeof(int64_t); }
 
 kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, const int32_t *next_pos, uint8_t label,

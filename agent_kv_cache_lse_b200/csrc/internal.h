@@ -122,6 +122,8 @@ cudaError_t launch_decode(const CacheView &c, const void *q, const int32_t *q_po
 cudaError_t launch_step_scores(const CacheView &c, const float *scores, const int32_t *step_start,
                                const int32_t *num_steps, int32_t max_steps, float beta, float *out, int32_t *status,
                                cudaStream_t stream);
+cudaError_t launch_push(int32_t *free_pages, int64_t free_capacity, int64_t *free_count, const int32_t *freed,
+                        int64_t freed_capacity, int64_t *num_freed, int32_t *status, cudaStream_t stream);
 cudaError_t launch_reserve(const CacheView &c, const int32_t *new_count, const int32_t *next_pos, uint8_t label, float *crf,
                            const int32_t *free_pages, int64_t free_capacity, const int64_t *free_count,
                            int32_t max_tokens, int32_t *row_len_out, int64_t *free_count_out, int32_t *token_start, int32_t *token_pos,

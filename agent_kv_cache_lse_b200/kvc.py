@@ -32,7 +32,7 @@ EXPORTS = ["kvc_status_string", "kvc_last_error", "kvc_version", "kvc_query_lse"
            "kvc_compact_pages", "kvc_compact_pages_noalloc", "kvc_ratchet_state_bytes", "kvc_ratchet_init",
            "kvc_confidence_ratchet", "kvc_beacon_update", "kvc_lrfu_select", "kvc_decode_attention",
            "kvc_step_scores", "kvc_append_workspace_bytes", "kvc_append_tokens", "kvc_select_plan",
-           "kvc_reserve_workspace_bytes", "kvc_reserve_slots", "kvc_norm_rope_write", "kvc_block_bounds",
+           "kvc_push_pages", "kvc_reserve_workspace_bytes", "kvc_reserve_slots", "kvc_norm_rope_write", "kvc_block_bounds",
            "kvc_select_blocks_workspace_bytes", "kvc_select_blocks", "kvc_block_attention_workspace_bytes",
            "kvc_block_attention"]
 
@@ -116,6 +116,7 @@ def lib() -> ctypes.CDLL:
             "kvc_append_workspace_bytes": (ctypes.c_size_t, [i32]),
             "kvc_append_tokens": (ctypes.c_int, [pc, vp, vp, vp, i32, ctypes.c_uint8, vp, vp, vp, vp, ctypes.c_size_t,
                                                  vp, vp]),
+            "kvc_push_pages": (ctypes.c_int, [vp, i64, vp, vp, i64, vp, vp, vp]),
             "kvc_reserve_workspace_bytes": (ctypes.c_size_t, [i32]),
             "kvc_reserve_slots": (ctypes.c_int, [vp, vp, vp, ctypes.c_uint8, vp, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp,
                                                  ctypes.c_size_t, vp, vp]),
@@ -471,6 +472,15 @@ def _call(name: str, dev: int, stream, *args):
     status = getattr(_lib or lib(), name)(*args, st)
     if status != KVC_OK:
         _check(status, name)
+
+
+def kvc_push_pages(free_pages: torch.Tensor, free_count: torch.Tensor, freed: torch.Tensor, num_freed: torch.Tensor,
+                   d_status=None, stream=None):
+    """Push the num_freed pages of a compaction's freed list onto the stack free_pages (depth free_count); num_freed becomes 0."""
+    dev = free_pages.get_device()
+    _call("kvc_push_pages", dev, stream, _arg(free_pages, "free_pages", (free_pages.numel(),), _I32, dev), free_pages.numel(),
+          _arg(free_count, "free_count", (1,), _I64, dev), _arg(freed, "freed", (freed.numel(),), _I32, dev), freed.numel(),
+          _arg(num_freed, "num_freed", (1,), _I64, dev), _opt(d_status, "d_status", (2,), _I32, dev))
 
 
 def kvc_reserve_workspace_bytes(rows: int) -> int:

@@ -7,9 +7,10 @@ matter for it.
   decode:  extend with one token for each sequence -> kvc_select_blocks -> kvc_block_attention
 
 (without a page budget, top_k = 0, decode attends to whole rows and keeps no bounds).  Nothing here computes; it allocates
-with torch and marshals arguments.  The free-page stack may be the freed list of an ``EvictionRound`` (its ``freed`` and
-``num_freed``), so that pages go round between eviction and new tokens; after a compaction, which moves entries
-between pages, call ``refresh``.  All calls take device tensors and do not synchronise, so a step can be captured into a
+with torch and marshals arguments.  After a compaction, which frees pages and moves entries between the others, call ``reclaim``
+with its freed list: the pages go back on the stack, so that they go round between eviction and new tokens, and the bounds are
+taken anew.  The freed list of an ``EvictionRound`` (its ``freed`` and ``num_freed``) can be the stack itself only until
+that round runs again: a compaction begins its list anew, and what is left on it would be lost.  All calls take device tensors and do not synchronise, so a step can be captured into a
 CUDA graph; two graphs of one ServingStep share its buffers and must not overlap.  A call whose arguments are refused
 (kvc.KvcError) is refused before anything is enqueued: the cache and the stack are as they were.
 """
@@ -107,6 +108,11 @@ class ServingStep:
         """Bounds of all pages (after a compaction, or when the cache was filled some other way)."""
         if self.top_k:
             kvc.kvc_block_bounds(self.cache, self.bounds, self.block_pos, None, self.status, stream)
+
+    def reclaim(self, freed: torch.Tensor, num_freed: torch.Tensor, stream=None):
+        """After a compaction: its freed pages go on the stack (num_freed becomes 0), and all pages' bounds are taken anew."""
+        kvc.kvc_push_pages(self.free_pages, self.free_count, freed, num_freed, self.status, stream)
+        self.refresh(stream)
 
     def extend(self, qkv: torch.Tensor, new_count: torch.Tensor, next_pos: torch.Tensor, label: int = 0, stream=None):
         """new_count[s] tokens of each sequence, packed in qkv [T][L][Hq + 2 Hkv][D] (T at most max_tokens; rows past

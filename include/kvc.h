@@ -328,7 +328,7 @@ size_t kvc_append_workspace_bytes(int32_t rows);
  * pages of the call) and enters it in its block table; slot_pos = new_pos of the row's sequence,
  * slot_label = label, crf (when not NULL) = 0 for the new slots; row_len += count; *free_count -= total.
  * k_new, v_new: [rows][count][head_dim] in the cache dtype, 16-byte aligned; new_pos: [num_seqs][count]
- * int32; free_pages: the stack (e.g. kvc_compact_pages' freed list), *free_count (device int64, in/out) its
+ * int32; free_pages: the stack (e.g. kvc_compact_pages' freed list, until its next call; see kvc_push_pages), *free_count (device int64, in/out) its
  * depth; workspace: kvc_append_workspace_bytes(rows) bytes of device memory.
  * Device faults: a stack too shallow for the call appends nothing and reports KVC_DEV_FREED_OVERFLOW
  * (row -1); a row that would exceed max_slots, or whose row_len is negative, is left alone and reported.
@@ -336,6 +336,19 @@ size_t kvc_append_workspace_bytes(int32_t rows);
 kvc_status kvc_append_tokens(const kvc_cache *cache, const void *k_new, const void *v_new, const int32_t *new_pos,
                              int32_t count, uint8_t label, float *crf, int32_t *free_pages, int64_t *free_count,
                              void *workspace, size_t workspace_bytes, int32_t *d_status, kvc_stream_t stream);
+
+/*
+ * The pages that a compaction freed go back on a free-page stack: free_pages[depth + i] = freed[i] for i < *num_freed,
+ * *free_count += *num_freed, *num_freed = 0 (so that no page is pushed twice).  kvc_compact_pages begins its list anew
+ * with every call; a stack that kvc_append_tokens and kvc_reserve_slots take pages from over several compactions is an
+ * array of its own, and takes each list over before the next compaction.
+ * free_pages: [free_capacity] int32, free_count (device int64, in/out) its depth; freed: [freed_capacity] int32, num_freed
+ * (device int64, in/out): as kvc_compact_pages writes them.  The two may not overlap.
+ * Device fault: a depth outside [0, free_capacity], a num_freed outside [0, freed_capacity] (a list that overflowed) or a
+ * stack without room for all pages pushes nothing and leaves both counts (KVC_DEV_FREED_OVERFLOW, row -1).
+ */
+kvc_status kvc_push_pages(int32_t *free_pages, int64_t free_capacity, int64_t *free_count, const int32_t *freed,
+                          int64_t freed_capacity, int64_t *num_freed, int32_t *d_status, kvc_stream_t stream);
 
 /* bytes of device workspace kvc_reserve_slots needs for `rows` rows */
 size_t kvc_reserve_workspace_bytes(int32_t rows);

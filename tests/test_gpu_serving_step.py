@@ -218,3 +218,59 @@ def test_a_refused_call_changes_nothing():
     st.decode(x, next_pos)
     torch.cuda.synchronize()
     assert st.device_status()[0] == 0 and c.row_len.tolist() == [101, 32, 65, 8]
+
+
+@pytest.mark.parametrize("n", [0, 1, 300, 100_003])
+def test_push(n):
+    """A list on top of a stack, counts moved over; a second push finds nothing; what does not fit stays where it is."""
+    cap, depth = n + 20, 20
+    stack = torch.arange(cap, dtype=I32, device=DEV)
+    freed = torch.arange(n + 7, dtype=I32, device=DEV) + 5_000_000
+    fc, nf, st = (torch.tensor(x, device=DEV) for x in ([depth], [n], [0, 0]))
+    st = st.to(I32)
+    for _ in range(2):
+        kvc.kvc_push_pages(stack, fc, freed, nf, st)
+        torch.cuda.synchronize()
+        assert int(fc[0]) == depth + n and int(nf[0]) == 0 and int(st[0]) == 0
+        assert stack.tolist() == list(range(depth)) + list(range(5_000_000, 5_000_000 + n))
+    kept = stack.clone()
+    for d, m in ((cap - 2, 3), (-1, 1), (cap + 1, 0), (0, -1), (0, n + 8)):
+        st.zero_()
+        fc.fill_(d)
+        nf.fill_(m)
+        kvc.kvc_push_pages(stack, fc, freed, nf, st)
+        torch.cuda.synchronize()
+        assert st.tolist() == [5, -1] and int(fc[0]) == d and int(nf[0]) == m and torch.equal(stack, kept)
+
+
+@pytest.mark.parametrize("top_k", [0, 4])
+def test_pages_go_round_over_several_evictions(top_k):
+    """Evict, decode, evict, decode, ...: every page is in one row or once on the stack, whatever was left on it."""
+    spec = synth.batch16(num_seqs=3, num_layers=2, lo=300, hi=700)
+    w = helpers.build(spec, DEV)
+    c, G, D, P = w.cache, spec.group, spec.head_dim, 16
+    rnd = EvictionRound(c)
+    rnd.budget.copy_(torch.tensor([64, 113, 160], dtype=I32, device=DEV))
+    num = c.k_pool.shape[0]
+    held = lambda: [p for r in range(c.rows) for p in c.block_table[r, : -(-int(c.row_len[r]) // P)].tolist()]
+    free = sorted(set(range(num)) - set(held()))
+    stack = torch.full((num,), -7, dtype=I32, device=DEV)
+    stack[: len(free)] = torch.tensor(free, dtype=I32, device=DEV)
+    count = torch.tensor([len(free)], device=DEV)
+    st = step.ServingStep(c, spec.num_q_heads, 3, stack, count, top_k=top_k, inv_freq=inv_freq(D), crf=rnd.crf)
+    next_pos = torch.tensor(spec.ctx, dtype=I32, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    for cycle in range(4):
+        rnd.run(w.queries, None, score_flags=kvc.KVC_SCORE_COMPUTE_LSE)
+        st.reclaim(rnd.freed, rnd.num_freed)
+        for i in range(5 + 20 * cycle):
+            qkv = torch.randn((3, 2, spec.num_q_heads + 16, D), device=DEV, generator=gen).to(torch.bfloat16)
+            st.decode(qkv, next_pos)
+            next_pos += 1
+        torch.cuda.synchronize()
+        assert rnd.device_status()[0] == 0 and st.device_status()[0] == 0
+        pages = held() + stack[: int(count[0])].tolist()
+        assert len(pages) == num and sorted(pages) == list(range(num))
+    if top_k:
+        check_select(c, st.bounds, st.block_pos, st.q[:3], next_pos - 1, 4, 1, 2)
+    check_attention(c, st.q[:3], next_pos - 1, *((st.block_list, st.block_count) if top_k else ()), rows=[0, 11, 23, 47])

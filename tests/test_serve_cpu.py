@@ -136,3 +136,22 @@ def test_binding_checks():
         kvc.kvc_block_attention(cache, q, qp, out.to(bf), lse, ws)
     with pytest.raises(kvc.KvcError, match="CUDA"):
         kvc.kvc_block_attention(cache, q, qp, out, lse, ws, li, n)
+
+
+def test_push_refusals():
+    L = kvc.lib()
+    G = ctypes.c_void_p(4096)
+
+    def call(fp=F, cap=9, fc=F, fr=G, n=5, nf=G):
+        return L.kvc_push_pages(fp, cap, fc, fr, n, nf, None, None)
+    for name in ("fp", "fc", "fr", "nf"):
+        assert call(**{name: None}) == BAD, name
+    assert call(cap=-1) == BAD and call(n=-1) == BAD and call(nf=F) == BAD
+    assert call(fr=F) == BAD and call(fr=ctypes.c_void_p(256 + 32)) == BAD and call(fp=ctypes.c_void_p(4096 + 16)) == BAD
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)
+    one = z(1, dt=torch.int64)
+    for a, text in (((z(9), z(1), z(5), one), "free_count: dtype"), ((z(9), one, z(5).long(), one), "freed: dtype"),
+                    ((z(9), one, z(5, 2)[:, 0], one), "contiguous"), ((z(9), one, z(5), z(2, dt=torch.int64)), "num_freed: shape"),
+                    ((z(9), one, z(5), one.clone()), "CUDA")):
+        with pytest.raises(kvc.KvcError, match=text):
+            kvc.kvc_push_pages(*a)
