@@ -3,6 +3,7 @@
 
 #include <cstdint>
 #include <cuda_runtime.h>
+#include <mutex>
 
 #include "../../include/kvc.h"
 
@@ -27,15 +28,19 @@ inline int device_sms() {
 
 // Raise a kernel's dynamic shared-memory limit to at least `bytes` on the current device; `done` (one array per
 // kernel, kMaxDevices entries, zero-initialised) remembers what each device was given, so the attribute is set
-// only when a call needs more than before.
+// only when a call needs more than before.  The attribute is set, not raised, so two host threads that both find the old
+// value may not set theirs in turn: the smaller could come last, under the larger one's launch.
 inline cudaError_t dyn_smem_at_least(const void *kernel, size_t bytes, int *done) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    int &have = done[dev & (kMaxDevices - 1)];
-    if ((size_t)have >= bytes) return cudaSuccess;
+    int *have = &done[dev & (kMaxDevices - 1)];
+    if ((size_t)__atomic_load_n(have, __ATOMIC_ACQUIRE) >= bytes) return cudaSuccess;
+    static std::mutex setting;
+    std::lock_guard<std::mutex> lock(setting);
+    if ((size_t)*have >= bytes) return cudaSuccess;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) have = (int)bytes;
+    if (e == cudaSuccess) __atomic_store_n(have, (int)bytes, __ATOMIC_RELEASE);
     return e;
 }
 
