@@ -385,8 +385,9 @@ kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, c
                              kvc_stream_t stream) {
     g_err[0] = 0;
     kvc::CacheView c;
-    kvc_status s = view_cache(cache, c, true);
+    kvc_status s = view_cache(cache, c, false);
     if (s != KVC_OK) return s;
+    if (c.num_pages <= 0 || c.num_pages > (int64_t)INT32_MAX) return fail(KVC_ERR_INVALID_ARGUMENT, "num_pages out of range");
     if (!new_count || !next_pos || !free_pages || !free_count)
         return fail(KVC_ERR_INVALID_ARGUMENT, "new_count, next_pos, free_pages and free_count are required");
     if (max_tokens < 0 || free_capacity < 0)

@@ -368,7 +368,7 @@ size_t kvc_reserve_workspace_bytes(int32_t rows);
  *       row_len_out  [rows] int32: the new lengths; may be cache->row_len itself.
  *       free_count_out  device int64: the new depth; may be free_count itself.
  * In/out: the cache's block_table (entries of new pages), slot_pos and slot_label (`label`), and crf
- *       ([rows][max_slots] fp32, may be NULL; 0) of the new slots.  k_pool and v_pool are not touched.
+ *       ([rows][max_slots] fp32, may be NULL; 0) of the new slots.  k_pool and v_pool are not used and may be NULL.
  * Device faults: more than max_tokens tokens (KVC_DEV_BAD_LENGTH, row -1), or a stack too shallow or
  * a depth outside [0, free_capacity] (KVC_DEV_FREED_OVERFLOW, row -1), reserve nothing: row_len_out and free_count_out get the old values and the slot
  * map -1 throughout.  A row is left alone and its slots are -1 when it would exceed max_slots

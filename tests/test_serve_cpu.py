@@ -155,3 +155,14 @@ def test_push_refusals():
                     ((z(9), one, z(5), one.clone()), "CUDA")):
         with pytest.raises(kvc.KvcError, match=text):
             kvc.kvc_push_pages(*a)
+
+
+def test_reserve_asks_for_no_pools():
+    """Slots are reserved in the tables alone: the checks after the cache's are reached without pools (num_pages still counts)."""
+    L = kvc.lib()
+
+    def call(**kw):
+        return L.kvc_reserve_slots(ctypes.byref(fake_cache(k_pool=None, v_pool=None, **kw)), F, F, 1, None, F, 9, F, 4, F, F, F, F,
+                                   F, F, 8, None, None)
+    assert call() == BAD and b"workspace" in L.kvc_last_error()
+    assert call(num_pages=0) == BAD and b"num_pages" in L.kvc_last_error()
