@@ -388,10 +388,10 @@ kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, c
     kvc_status s = view_cache(cache, c, false);
     if (s != KVC_OK) return s;
     if (c.num_pages <= 0 || c.num_pages > (int64_t)INT32_MAX) return fail(KVC_ERR_INVALID_ARGUMENT, "num_pages out of range");
-    if (!new_count || !next_pos || !free_pages || !free_count)
-        return fail(KVC_ERR_INVALID_ARGUMENT, "new_count, next_pos, free_pages and free_count are required");
     if (max_tokens < 0 || free_capacity < 0)
         return fail(KVC_ERR_INVALID_ARGUMENT, "max_tokens and free_capacity must be >= 0");
+    if (!new_count || !next_pos || !free_count || (free_capacity > 0 && !free_pages))
+        return fail(KVC_ERR_INVALID_ARGUMENT, "new_count, next_pos, free_pages and free_count are required");
     if (!row_len_out || !free_count_out || !token_start || (max_tokens > 0 && (!token_pos || !slot_map)))
         return fail(KVC_ERR_INVALID_ARGUMENT,
                     "row_len_out, free_count_out, token_start, token_pos and slot_map are required");

@@ -360,7 +360,7 @@ size_t kvc_reserve_workspace_bytes(int32_t rows);
  * one from the top of the free-page stack, in the order of kvc_append_tokens: row r's k-th new page is
  * free_pages[depth - total + offset_r + k], offset_r the pages all lower rows take, total the pages of the call.
  * In:   new_count, next_pos [num_seqs] int32 (next_pos: the position of the sequence's first new token);
- *       free_pages [free_capacity], free_count (device int64: the stack's depth); max_tokens: the size of token_pos and slot_map.
+ *       free_pages [free_capacity] (NULL where that is 0), free_count (device int64: the stack's depth); max_tokens: the size of token_pos and slot_map.
  * Out:  token_start  [num_seqs + 1] int32: where each sequence's tokens begin, and the number of tokens.
  *       token_pos    [max_tokens] int32: each token's position (-1 past the last token).
  *       slot_map     [max_tokens][num_layers][num_kv_heads] int64: page * page_size + offset of the token's

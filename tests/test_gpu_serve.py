@@ -624,3 +624,21 @@ def test_select_one_page_past_fp32_among_ordinary_ones(dtype):
     pos, qp = torch.zeros((1, mp), dtype=I32, device=DEV), torch.zeros(1, dtype=I32, device=DEV)
     for k in (1, 7, 39):
         check_select(c, b.to(DT[dtype]), pos, q.to(DT[dtype]), qp, k)
+
+
+def test_reserve_with_a_stack_of_no_entries():
+    """Tokens that fit the pages a row holds need none; a row that needs one refuses the call."""
+    c, _ = cache_of([5, 17], 16, 64, "bf16", 1, 1, 2, seed=3, device=DEV)
+    before = c.block_table.clone()
+    for new, want in ((3, 0), (12, 5)):
+        st, z = status(), lambda *s, dt=I32: torch.zeros(s, dtype=dt, device=DEV)
+        sm, old = z(new, 1, 2, dt=torch.int64), c.row_len.tolist()
+        kvc.kvc_reserve_slots(c, torch.tensor([new], dtype=I32, device=DEV), z(1), 0, None, z(0), z(1, dt=torch.int64), c.row_len,
+                              z(1, dt=torch.int64), z(2), z(new), sm, words(kvc.kvc_reserve_workspace_bytes(2)), st)
+        assert code(st) == want
+        if want:
+            assert c.row_len.tolist() == old and (sm == -1).all()
+        else:
+            assert c.row_len.tolist() == [n + new for n in old]
+            assert sm[:, 0].tolist() == [[int(before[r, n // 16]) * 16 + n % 16 + i for r, n in enumerate(old)] for i in range(new)]
+    assert torch.equal(c.block_table, before)

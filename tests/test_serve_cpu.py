@@ -166,3 +166,13 @@ def test_reserve_asks_for_no_pools():
                                    F, F, 8, None, None)
     assert call() == BAD and b"workspace" in L.kvc_last_error()
     assert call(num_pages=0) == BAD and b"num_pages" in L.kvc_last_error()
+
+
+def test_reserve_takes_a_stack_without_room():
+    """A stack of no entries (a torch tensor of size 0 has no address) serves steps that need no page."""
+    L = kvc.lib()
+
+    def call(fp, cap):
+        return L.kvc_reserve_slots(ctypes.byref(fake_cache()), F, F, 1, None, fp, cap, F, 4, F, F, F, F, F, F, 8, None, None)
+    assert call(None, 1) == BAD and b"free_pages" in L.kvc_last_error()
+    assert call(None, 0) == BAD and b"workspace" in L.kvc_last_error()
