@@ -397,7 +397,7 @@ _CACHE = struct.Struct("@PPqiiiiPPPPiiii")
 assert _CACHE.size == ctypes.sizeof(KvcCache)
 _DTYPE = {torch.float32: KVC_F32, torch.bfloat16: KVC_BF16}
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a torch without CUDA has none, and no call to make
 
 
 def _arg(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
