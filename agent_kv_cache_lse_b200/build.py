@@ -11,6 +11,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvc.so")
 BIND = os.path.join(HERE, "_bind.so")  # csrc/bind.cpp, loaded by kvc.py
+BIND_FOR = os.path.join(HERE, "_build", "bind_for.txt")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
@@ -20,9 +21,19 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _bind_target() -> str:
+    """The torch and interpreter that _bind.so is compiled for (kept beside its build in BIND_FOR)."""
+    import torch
+
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+    if not os.path.exists(LIB) or not os.path.exists(BIND) or not os.path.exists(BIND_FOR):
         return False
+    with open(BIND_FOR) as f:
+        if f.read() != _bind_target():
+            return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
     deps = sources() + [os.path.join(CSRC, "bind.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
     deps.append(os.path.join(HERE, "..", "include", "kvc.h"))
@@ -54,6 +65,8 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
         raise RuntimeError("link failed:\n" + out.stdout)
     os.replace(tmp, LIB)
     os.replace(BIND + ".tmp", BIND)
+    with open(BIND_FOR, "w") as f:
+        f.write(_bind_target())
     return LIB
 
 
@@ -66,7 +79,7 @@ def _start_bind(out: str):
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKVC_TORCH="{torch.__version__}"',
            f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
            f"-I{sysconfig.get_paths()['include']}", "-o", out, os.path.join(CSRC, "bind.cpp"), f"-L{root}/lib",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{root}/lib"]

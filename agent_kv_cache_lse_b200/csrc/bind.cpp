@@ -14,7 +14,9 @@
 #include <dlfcn.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cstring>
 #include <initializer_list>
+#include <string>
 
 #include "../../include/kvc.h"
 
@@ -309,9 +311,30 @@ PyMethodDef methods[] = {
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
+// Torch's tensor layout and the interpreter's are compiled in, so the module loads only into those it was built for (KVC_TORCH:
+// the version of torch).
+bool built_for_this() {
+    const std::string python = std::to_string(PY_MAJOR_VERSION) + "." + std::to_string(PY_MINOR_VERSION) + ".";
+    if (std::strncmp(Py_GetVersion(), python.c_str(), python.size()) != 0) return false;
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    PyObject *text = version ? PyObject_Str(version) : nullptr;
+    const char *have = text ? PyUnicode_AsUTF8(text) : nullptr;
+    const bool same = have && std::strcmp(have, KVC_TORCH) == 0;
+    Py_XDECREF(text);
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    PyErr_Clear();
+    return same;
+}
+
 }  // namespace
 
 PyMODINIT_FUNC PyInit__bind(void) {
+    if (!built_for_this()) {
+        PyErr_SetString(PyExc_ImportError, "_bind.so was built for torch " KVC_TORCH " and another interpreter or torch is running");
+        return nullptr;
+    }
     struct {
         PyObject **to;
         const char *name;
