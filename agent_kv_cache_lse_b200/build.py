@@ -28,28 +28,44 @@ def _bind_target() -> str:
     return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND) or not os.path.exists(BIND_FOR):
+def _newer(target: str, deps) -> bool:
+    deps = list(deps) + [os.path.join(HERE, "..", "include", "kvc.h")]
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps if os.path.exists(d))
+
+
+def lib_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")))
+
+
+def bind_up_to_date() -> bool:
+    if not _newer(BIND, [os.path.join(CSRC, "bind.cpp")]) or not os.path.exists(BIND_FOR):
         return False
     with open(BIND_FOR) as f:
-        if f.read() != _bind_target():
-            return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BIND))
-    deps = sources() + [os.path.join(CSRC, "bind.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-    deps.append(os.path.join(HERE, "..", "include", "kvc.h"))
-    return all(os.path.getmtime(d) <= t for d in deps if os.path.exists(d))
+        return f.read() == _bind_target()
+
+
+def up_to_date() -> bool:
+    return lib_up_to_date() and bind_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libkvc.so, and compile _bind.so; returns the library's path."""
+    """Compile every csrc/*.cu for sm_100a and link libkvc.so, and compile _bind.so; returns the library's path.  The library is all
+    that is needed: where _bind.so does not compile (no headers of torch or Python), that is said and the Python path is left."""
     if not force and up_to_date():
         return LIB
-    objdir = os.path.join(HERE, "_build")
-    os.makedirs(objdir, exist_ok=True)
+    os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
+    bind = None if not force and bind_up_to_date() else _start_bind(BIND + ".tmp")
+    if force or not lib_up_to_date():
+        _build_lib(verbose, jobs)
+    if bind is not None:
+        _finish_bind(bind)
+    return LIB
+
+
+def _build_lib(verbose: bool, jobs: int):
     procs, objs = [], []
-    procs.append(("bind.cpp", _start_bind(BIND + ".tmp")))
     for src in sources():
-        obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
+        obj = os.path.join(HERE, "_build", os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         cmd = [NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj]
         if verbose:
@@ -64,14 +80,10 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 8) -> str:
     if out.returncode != 0:
         raise RuntimeError("link failed:\n" + out.stdout)
     os.replace(tmp, LIB)
-    os.replace(BIND + ".tmp", BIND)
-    with open(BIND_FOR, "w") as f:
-        f.write(_bind_target())
-    return LIB
 
 
 def _start_bind(out: str):
-    """Compile csrc/bind.cpp against torch's headers and libraries (those of the interpreter that builds)."""
+    """Start compiling csrc/bind.cpp against torch's headers and libraries (those of the interpreter that builds)."""
     import sysconfig
 
     import torch
@@ -83,7 +95,24 @@ def _start_bind(out: str):
            f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
            f"-I{sysconfig.get_paths()['include']}", "-o", out, os.path.join(CSRC, "bind.cpp"), f"-L{root}/lib",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{root}/lib"]
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    except OSError as e:
+        return e
+
+
+def _finish_bind(proc):
+    """Put _bind.so in its place, or, if it did not compile, say so and leave none (an older one may not fit the library)."""
+    out = str(proc) if isinstance(proc, OSError) else proc.communicate()[0]
+    if not isinstance(proc, OSError) and proc.returncode == 0:
+        os.replace(BIND + ".tmp", BIND)
+        with open(BIND_FOR, "w") as f:
+            f.write(_bind_target())
+        return
+    for path in (BIND, BIND_FOR):
+        if os.path.exists(path):
+            os.remove(path)
+    sys.stderr.write("_bind.so was not built (calls are packed in Python instead):\n" + out + "\n")
 
 
 def _reap(procs, verbose):

@@ -40,3 +40,17 @@ def test_the_build_looks_at_the_torch_it_was_made_for(monkeypatch, tmp_path):
     assert build.up_to_date()
     monkeypatch.setattr(torch, "__version__", "1.0.0")
     assert not build.up_to_date()
+
+
+@pytest.mark.parametrize("cxx", ["/nonexistent/g++", "false"])
+def test_the_library_builds_without_a_host_compiler_for_the_native_module(monkeypatch, tmp_path, capfd, cxx):
+    from agent_kv_cache_lse_b200 import build
+    lib = tmp_path / "libkvc.so"
+    lib.write_text("")
+    os.utime(lib, (4e9, 4e9))
+    (tmp_path / "_bind.so").write_text("older")
+    for name, path in (("LIB", lib), ("BIND", tmp_path / "_bind.so"), ("BIND_FOR", tmp_path / "bind_for.txt")):
+        monkeypatch.setattr(build, name, str(path))
+    monkeypatch.setenv("CXX", cxx)
+    assert build.build() == str(lib)
+    assert "_bind.so was not built" in capfd.readouterr().err and not (tmp_path / "_bind.so").exists()
