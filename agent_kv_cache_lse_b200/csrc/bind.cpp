@@ -160,13 +160,14 @@ struct Call {
     kvc_stream_t stream(PyObject *o) {
         if (!ok) return nullptr;
         if (o == Py_None) return (kvc_stream_t)c10::cuda::getCurrentCUDAStream(dev).stream();
-        if (PyLong_Check(o)) return (kvc_stream_t)PyLong_AsVoidPtr(o);
-        PyObject *h = attr(o, s_stream, 9);
+        PyObject *h = PyLong_Check(o) ? o : attr(o, s_stream, 9);
         if (!h || !PyLong_Check(h)) {
             ok = false;
             return nullptr;
         }
-        return (kvc_stream_t)PyLong_AsVoidPtr(h);
+        const unsigned long long s = PyLong_AsUnsignedLongLong(h);
+        if (s == ~0ull && PyErr_Occurred()) ok = false;  // negative, or past 64 bits
+        return (kvc_stream_t)(uintptr_t)s;
     }
 };
 

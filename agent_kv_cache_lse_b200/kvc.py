@@ -469,6 +469,8 @@ def _call(name: str, dev: int, stream, *args):
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
     st = _raw_stream(dev) if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if not 0 <= st < 1 << 64:
+        raise KvcError(f"stream: {st} is no stream")
     status = getattr(_lib or lib(), name)(*args, st)
     if status != KVC_OK:
         _check(status, name)

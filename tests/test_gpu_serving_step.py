@@ -274,3 +274,20 @@ def test_pages_go_round_over_several_evictions(top_k):
     if top_k:
         check_select(c, st.bounds, st.block_pos, st.q[:3], next_pos - 1, 4, 1, 2)
     check_attention(c, st.q[:3], next_pos - 1, *((st.block_list, st.block_count) if top_k else ()), rows=[0, 11, 23, 47])
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_a_number_that_is_no_stream_is_refused(monkeypatch, native):
+    c, _ = cache_of([40], 16, 64, "f32", 1, 1, 1, seed=8, device=DEV)
+    mp = c.block_table.shape[1]
+    b, pos = torch.zeros((1, mp, 2, 64), device=DEV), torch.full((1, mp), 7, dtype=I32, device=DEV)
+    if not native:
+        monkeypatch.setattr(kvc, "_bind", None)
+    for bad in (1 << 70, -(1 << 70), -1):
+        with pytest.raises(kvc.KvcError, match="no stream"):
+            kvc.kvc_block_bounds(c, b, pos, stream=bad)
+    torch.cuda.synchronize()
+    assert (pos == 7).all()
+    kvc.kvc_block_bounds(c, b, pos, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    assert (pos[0, :3] < 7).any()
