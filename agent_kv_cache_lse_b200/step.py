@@ -104,6 +104,13 @@ class ServingStep:
         if not 0 <= label <= 255:
             raise kvc.KvcError(f"label: {label}, expected 0 to 255")
 
+    def _stream(self, stream):
+        """The stream of a call as torch has it: the cache's device's current one for None, and a handle's for a number."""
+        dev = self.cache.k_pool.device
+        if stream is None:
+            return torch.cuda.current_stream(dev)
+        return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
+
     def refresh(self, stream=None):
         """Bounds of all pages (after a compaction, or when the cache was filled some other way)."""
         if self.top_k:
@@ -122,7 +129,7 @@ class ServingStep:
 
     def _extend(self, qkv, new_count, next_pos, label, stream):
         c, T = self.cache, qkv.shape[0]
-        main = stream if stream is not None else torch.cuda.current_stream(c.k_pool.device)
+        main = self._stream(stream)
         with torch.cuda.stream(main):
             self.old_len.copy_(c.row_len)
         kvc.kvc_reserve_slots(c, new_count, next_pos, label, self.crf, self.free_pages, self.free_count, c.row_len,
@@ -144,7 +151,7 @@ class ServingStep:
         self._check_call(qkv, self.ones, next_pos, label)
         if qkv.shape[0] < S:
             raise kvc.KvcError(f"qkv: {qkv.shape[0]} tokens, expected one for each of {S} sequences")
-        main = stream if stream is not None else torch.cuda.current_stream(c.k_pool.device)
+        main = self._stream(stream)
         self._extend(qkv, self.ones, next_pos, label, main)
         q, pages = self.q[:S], None
         if self.top_k:

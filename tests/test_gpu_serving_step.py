@@ -291,3 +291,24 @@ def test_a_number_that_is_no_stream_is_refused(monkeypatch, native):
     kvc.kvc_block_bounds(c, b, pos, stream=torch.cuda.Stream())
     torch.cuda.synchronize()
     assert (pos[0, :3] < 7).any()
+
+
+@pytest.mark.parametrize("top_k", [0, 3])
+def test_a_step_on_a_stream_given_by_its_handle(top_k):
+    """As the entry points, the step takes a stream object or its address; a step on each of them gives the same."""
+    def go(stream):
+        c, free = cache_of([90, 31, 64, 70], 16, 64, "bf16", 2, 1, 2, seed=8, spare=9, extra_pages=3, device=DEV)
+        s = step.ServingStep(c, 4, 2, free.to(DEV), torch.tensor([len(free)], device=DEV), top_k=top_k, inv_freq=inv_freq(32))
+        x = torch.randn((2, 1, 8, 64), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(torch.bfloat16)
+        pos, freed = torch.tensor([90, 70], dtype=I32, device=DEV), torch.zeros((0,), dtype=I32, device=DEV)
+        none = torch.zeros(1, dtype=torch.int64, device=DEV)
+        torch.cuda.synchronize()
+        s.decode(x, pos, stream=stream)
+        s.reclaim(freed, none, stream=stream)
+        torch.cuda.synchronize()
+        assert s.device_status()[0] == 0
+        return s.out, s.lse, c.k_pool, c.row_len
+    side = torch.cuda.Stream()
+    want = go(None)
+    for stream in (side, side.cuda_stream, 0):
+        assert all(torch.equal(x, y) for x, y in zip(want, go(stream)))
