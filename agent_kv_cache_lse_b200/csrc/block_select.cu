@@ -5,8 +5,7 @@
 //     score_b = sum_d (sum_g max(q_gd, 0)) hi_bd + (sum_g min(q_gd, 0)) lo_bd = sum_d up_d hi_bd + down_d lo_bd,
 // one dot product of 2 D terms a page whatever the group's size.  Which pages are chosen is a whole number, and with 32
 // bits two orders of summation would choose differently at the border, so the choice is that of the scores in 64 bits.
-// A bound that is not finite always makes the sum NaN or +inf (0 * inf, or inf - inf, where the factors' signs do
-// not), and NaN ranks as +inf.
+// A page with a bound that is not finite ranks as +inf, like one whose score is NaN, whatever the factors' signs make of it.
 //
 // 64-bit arithmetic for every page took 80 instructions a page and warp and 1.4 times the time of the bytes.  But only pages
 // at the border need it.  With x in 32 bits, of 8 multiply-adds a lane and 5 sums across lanes on factors rounded once (14
@@ -443,7 +442,10 @@ __global__ void __launch_bounds__(kPickThreads, 2) block_pick_kernel(SelectArgs 
                     const int b = b0 + __ffs(todo) - 1;
                     const T *v = static_cast<const T *>(a.bounds) + (base + b) * 2 * D;
                     double s = 0;
-                    for (int i = lane; i < 2 * D; i += 32) s = fma(w[i], (double)static_cast<float>(v[i]), s);
+                    for (int i = lane; i < 2 * D; i += 32) {
+                        const float x = static_cast<float>(v[i]);
+                        s = isfinite(x) ? fma(w[i], (double)x, s) : __longlong_as_double(0x7ff8000000000000ll);  // NaN stays
+                    }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                     if (lane == 0) exact[b] = score_key(s);

@@ -642,3 +642,54 @@ def test_reserve_with_a_stack_of_no_entries():
             assert c.row_len.tolist() == [n + new for n in old]
             assert sm[:, 0].tolist() == [[int(before[r, n // 16]) * 16 + n % 16 + i for r, n in enumerate(old)] for i in range(new)]
     assert torch.equal(c.block_table, before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_rows_of_more_pages_than_a_cta_keeps(dtype, D):
+    """Rows of 20,000 and 16,385 pages (their keys do not fit a CTA's shared memory) beside one that just fits and a short one."""
+    c, _ = cache_of([20000, 16385, 16384, 70], 1, D, dtype, 4, 1, 1, seed=16, device=DEV, late=False)
+    rows, mp = c.block_table.shape
+    g = torch.Generator(device=DEV).manual_seed(D)
+    b = torch.randn((rows, mp, 2, D), device=DEV, generator=g).sort(2)[0].to(DT[dtype]).contiguous()
+    b[1, 5000:9000] = b[1, 5000]  # many ties
+    q = torch.randn((4, 1, 2, D), device=DEV, generator=g).to(DT[dtype])
+    pos = torch.randint(0, 10, (rows, mp), device=DEV, generator=g, dtype=I32)
+    for q_pos, k, sink, recent in ((9, 1, 0, 0), (9, 300, 1, 2), (4, 7000, 3, 100), (9, 25000, 0, 1)):
+        check_select(c, b, pos, q, torch.full((4,), q_pos, dtype=I32, device=DEV), k, sink, recent)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_bounds_that_are_not_finite(dtype, D):
+    """NaN and both infinities in every place of a word and lane, negative factors among the query's, and a query with a NaN."""
+    n = 200
+    c, _ = cache_of([n * 16, n * 16], 16, D, dtype, 2, 1, 1, seed=17, device=DEV, late=False)
+    mp = c.block_table.shape[1]
+    g = torch.Generator(device=DEV).manual_seed(D + 1)
+    b = torch.randn((2, mp, 2, D), device=DEV, generator=g).sort(2)[0].to(DT[dtype]).contiguous()
+    bad = [float("nan"), float("inf"), float("-inf")]
+    for i in range(40):
+        b[0, 3 + 4 * i, i % 2, (7 * i) % D] = bad[i % 3]
+    q = torch.randn((2, 1, 2, D), device=DEV, generator=g).to(DT[dtype])
+    q[1, 0, 1, 3] = float("nan")
+    pos, qp = torch.zeros((2, mp), dtype=I32, device=DEV), torch.zeros(2, dtype=I32, device=DEV)
+    for k in (1, 17, 40, 41, 120):
+        check_select(c, b, pos, q, qp, k)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_select_bf16_scores_that_32_bits_cannot_tell_apart(D):
+    """Pages that differ in one element with a tiny factor: by far less than fp32 resolves of the score."""
+    n = 600
+    c, _ = cache_of([n * 16], 16, D, "bf16", 1, 1, 1, seed=18, device=DEV, late=False)
+    mp = c.block_table.shape[1]
+    g = torch.Generator(device=DEV).manual_seed(D)
+    lo = torch.randn((D,), device=DEV, generator=g).repeat(1, mp, 1).to(torch.bfloat16)
+    lo[0, :, D // 2] = torch.randint(-100, 100, (mp,), device=DEV, generator=g).to(torch.bfloat16) / 64
+    b = torch.stack((lo, lo + 1), 2).contiguous()
+    q = torch.randn((1, 1, 3, D), device=DEV, generator=g)
+    q[..., D // 2] = torch.tensor([1e-9, -2e-9, 3e-10], device=DEV)
+    pos, qp = torch.zeros((1, mp), dtype=I32, device=DEV), torch.zeros(1, dtype=I32, device=DEV)
+    for k in (1, 17, 300, 599):
+        check_select(c, b, pos, q.to(torch.bfloat16), qp, k)
