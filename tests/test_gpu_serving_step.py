@@ -312,3 +312,38 @@ def test_a_step_on_a_stream_given_by_its_handle(top_k):
     want = go(None)
     for stream in (side, side.cuda_stream, 0):
         assert all(torch.equal(x, y) for x, y in zip(want, go(stream)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top_k", [0, 3])
+@pytest.mark.parametrize("weights", [True, False])
+def test_native_and_python_packing_make_the_same_calls(monkeypatch, dtype, top_k, weights):
+    """Every argument a step passes, optional ones among them, arrives the same either way, and a refusal says the same."""
+    w = (1 + 0.1 * torch.randn((2, 64), device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))).to(DT[dtype]) if weights else None
+
+    def go():
+        c, free = cache_of([90, 31, 64, 70, 1, 0, 16, 33], 16, 64, dtype, 2, 2, 2, seed=8, spare=20, extra_pages=4, device=DEV)
+        crf = torch.ones((8, c.max_slots), device=DEV)
+        s = step.ServingStep(c, 4, 40, free.to(DEV), torch.tensor([len(free)], device=DEV), top_k=top_k, q_weight=w, k_weight=w,
+                             eps=1e-5, inv_freq=inv_freq(48) if weights else None, interleaved=weights, crf=crf if weights else None)
+        if not weights:
+            c.slot_label = None
+        x = torch.randn((37, 2, 8, 64), device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(DT[dtype])
+        pos = torch.tensor([90, 70], dtype=I32, device=DEV)
+        s.extend(x, torch.tensor([30, 5], dtype=I32, device=DEV), pos, label=2)
+        s.decode(x[35:], pos + 40, label=1)
+        torch.cuda.synchronize()
+        assert s.device_status()[0] == 0
+        words = []
+        for bad in (dict(block_list=torch.zeros((8, 2), dtype=I32, device=DEV)), dict(out=s.out.to(torch.bfloat16)),
+                    dict(workspace=s.attend_ws[:1]), dict(q_pos=pos[:1])):
+            a = {**dict(q=s.q[:2], q_pos=pos, out=s.out, lse=s.lse, workspace=s.attend_ws), **bad}
+            with pytest.raises(kvc.KvcError) as e:
+                kvc.kvc_block_attention(c, **a)
+            words.append(str(e.value))
+        return [s.out, s.lse, s.q, s.slot_map, s.token_pos, s.token_start, s.free_count, crf, c.k_pool, c.v_pool, c.block_table,
+                c.row_len, c.slot_pos] + ([s.block_list, s.bounds, s.block_pos] if top_k else []), words
+    native = go()
+    monkeypatch.setattr(kvc, "_bind", None)
+    python = go()
+    assert native[1] == python[1] and all(torch.equal(x, y) for x, y in zip(native[0], python[0]))
