@@ -16,6 +16,7 @@ CUDA graph; two graphs of one ServingStep share its buffers and must not overlap
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Optional
 
@@ -105,11 +106,10 @@ class ServingStep:
             raise kvc.KvcError(f"label: {label}, expected 0 to 255")
 
     def _stream(self, stream):
-        """The stream of a call as torch has it: the cache's device's current one for None, and a handle's for a number."""
-        dev = self.cache.k_pool.device
-        if stream is None:
-            return torch.cuda.current_stream(dev)
-        return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
+        """The stream of a call as torch has it, and a handle's for a number (None: the current one of the cache's device)."""
+        if stream is None or hasattr(stream, "cuda_stream"):
+            return stream
+        return torch.cuda.ExternalStream(int(stream), device=self.cache.k_pool.device)
 
     def refresh(self, stream=None):
         """Bounds of all pages (after a compaction, or when the cache was filled some other way)."""
@@ -130,7 +130,7 @@ class ServingStep:
     def _extend(self, qkv, new_count, next_pos, label, stream):
         c, T = self.cache, qkv.shape[0]
         main = self._stream(stream)
-        with torch.cuda.stream(main):
+        with torch.cuda.stream(main) if main is not None else contextlib.nullcontext():
             self.old_len.copy_(c.row_len)
         kvc.kvc_reserve_slots(c, new_count, next_pos, label, self.crf, self.free_pages, self.free_count, c.row_len,
                               self.free_count, self.token_start, self.token_pos[:T], self.slot_map[:T], self.reserve_ws,
