@@ -22,9 +22,9 @@
 // A tensor-core step truncates when it adds to its accumulator, which over a run of hundreds of chunks drifts (7e-6 at 138
 // chunks), so each chunk's product starts from zero and is added to the run's output by a rounded fp32 addition.
 // fp32: a lane owns 8 elements of D of a key and all dot products are fp32 FMAs.
-// Measured (bf16, 8 KV heads, 4 query heads each): 219 us for 16 sequences of 8K to 33K slots (1.39 GB, 6.3 TB/s), 94 us for one of
-// 131,072, 35 us for 128 chosen pages of 16 sequences (136 MB): about 7 us pass before the first chunk is there, 5 at the end for
-// the joins, and the SMs end up to 10% apart.
+// Measured a call (bf16, 8 KV heads, 4 query heads each): 219 us for 16 sequences of 8K to 33K slots (1.39 GB, 6.3 TB/s), 95 us for
+// one of 131,072, 35 us for 128 chosen pages of 16 sequences (136 MB): a warp's first chunk is there after 6 to 7 us, the SMs' last
+// ones lie 12 to 19% apart, and the joins take 5 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -5,8 +5,8 @@
 // it, so a warp takes a page: D * sizeof(T) / 16 lanes cover a key row with 16 bytes each, and the warp's key groups
 // join with shuffles at the end.  A row's pages go round the warps of its CTAs; a warp looks its page ids up 32 at a
 // time and streams its keys through a ring of kRing stages of shared memory (kBatch key groups each) with cp.async.  A lane
-// reads back only what it copied itself.  Measured: 16.4 us for 8 rows of 32,768 keys (4.7 TB/s; with two stages of registers in
-// place of the ring 18.2), 4.0 us for the one or two changed pages of 1,024 rows (start-up alone).
+// reads back only what it copied itself.  Measured a call: 16.5 us for 8 rows of 32,768 keys (4.7 TB/s; with two stages of registers in
+// place of the ring 18.2), 4.3 us for the one or two changed pages of 1,024 rows (start-up alone).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -24,8 +24,8 @@
 //   digit in which the k-th key lies, usually with a handful of keys, which are ranked directly; while there are more than
 //   kFew, the next 11 bits follow.  The 64-bit scores between c - 2 e and c + 2 e, if they have to be ranked, go the same
 //   way.  One pass in index order then lists the pages.
-// Measured: 77 us for 677,000 pages of 512 rows (16 sequences of 8K to 33K tokens, 4 layers; 62 us launch A, 5.6 TB/s), 89 us with
-// 64-bit scores throughout; 11 us for 8 rows of 2,048 pages, of which the bytes are 1.3 (a dozen barriers of launch B the rest).
+// Measured a call: 77 us for 677,000 pages of 512 rows (16 sequences of 8K to 33K tokens, 4 layers; 62 us launch A, 5.6 TB/s), 89 us with
+// 64-bit scores throughout; 11 to 12 us for 8 rows of 2,048 pages, of which the bytes are 1.3 (a dozen barriers of launch B the rest).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -22,8 +22,9 @@
 // warp.  A warp takes its run in groups of up to kSteps steps of one kind, streamed through a ring of kRing stages of its
 // own with cp.async (a lane's registers then hold no loads in flight: with batches of loads in registers the kernel was
 // bound by occupancy or by spills).  When it comes to a new token it makes that token's rope_dim / 2 pairs (cos, sin) in
-// shared memory, and at a layer's queries and keys its C and S.  Measured: 148 us for 32,768 tokens of 32 + 2 x 8 heads of 128 (bf16,
-// 5.4 TB/s read and written, 57% of the issue slots), 3.4 us for 16 tokens, 10.6 us for 1,003 fp32 tokens of two layers (37 MB).
+// shared memory, and at a layer's queries and keys its C and S.  Measured a call: 153 us for 32,768 tokens of 32 + 2 x 8 heads of
+// 128 (bf16, 5.3 TB/s read and written, 52% of the issue slots), 3.7 us for 16 tokens, 10.2 us for 1,003 fp32 tokens of two
+// layers (37 MB).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -17,8 +17,9 @@
 //   scattered writes to the rows and a search of the sequence for each cell, took 29 us where this takes 12, both under the profiler).
 // The bytes are few; what counts is the chain of dependent loads and the launches.  A decode step's few cells are
 // filled by the planning CTA itself; else the fill is a second launch that is resident before the plan ends
-// (programmatic dependent launch).  Measured: 5.0 us for a decode step of 16 sequences (128 rows), 12.3 us for 28,049 prompt tokens
-// of 33 sequences in 1,056 rows (15.8 MB written, 2.4 us of them by bandwidth; the plan's and the fill's load chains are the rest).
+// (programmatic dependent launch).  Measured a call: 5.2 us for a decode step of 16 sequences (128 rows), 12.2 us for 28,049 prompt tokens
+// of 33 sequences in 1,056 rows (15.8 MB written, 2.4 us of them by bandwidth; the plan's and the fill's load chains, and
+// the fill's 5.3 M warp instructions, are the rest).
 #include <algorithm>
 
 #include "common.cuh"

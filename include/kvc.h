@@ -29,6 +29,7 @@
  *
  * Next to the path, one model step over the cache (its attention may read the whole row or only
  * the pages that a cheap score chooses):
+ *      kvc_push_pages          freed pages back on the free-page stack
  *      kvc_reserve_slots       pages, block-table entries and slot maps for the requests' new tokens
  *      kvc_norm_rope_write     per-head norms and position rotation of queries and keys, keys and
  *                              values written into the reserved slots
@@ -391,7 +392,8 @@ kvc_status kvc_reserve_slots(const kvc_cache *cache, const int32_t *new_count, c
  * and, over the first rope_dim elements, with f_j = token_pos * inv_freq[j], j < rope_dim / 2,
  *     (y_a, y_b) <- (y_a cos f_j - y_b sin f_j, y_a sin f_j + y_b cos f_j)
  * for (a, b) = (j, j + rope_dim / 2), or (2 j, 2 j + 1) with KVC_ROPE_INTERLEAVED.  Values are copied.  The
- * arithmetic is fp32 with one rounding at the end; the angle is taken in 64 bits, so far positions keep theirs.
+ * arithmetic is fp32 with one rounding at the end, the mean of squares in fp32's range; the angle is taken in 64 bits, so far
+ * positions keep theirs.
  * qkv:       [num_tokens] tokens, token_stride elements apart, of [num_layers][num_q_heads + 2 * num_kv_heads]
  *            [head_dim] in the cache's dtype: query heads, then key heads, then value heads.  16-byte aligned,
  *            token_stride a multiple of 16 bytes.
@@ -439,7 +441,7 @@ size_t kvc_select_blocks_workspace_bytes(int32_t rows, int32_t max_pages_per_row
  * (block_pos <= q_pos), the row's first sink_blocks and last recent_blocks pages are always taken, and the rest of
  * top_k goes to the highest scores, ties to the lower page index; a page whose bounds are not
  * finite, or whose score is NaN, ranks with +inf (so that attention shows such keys instead of passing over them).  The scores are taken in 64 bits, so the choice does not depend on the order of a sum.
- * bounds, block_pos: as kvc_block_bounds writes them.  q, q_pos: as for kvc_decode_attention.
+ * bounds, block_pos: as kvc_block_bounds writes them (lo <= hi).  q, q_pos: as for kvc_decode_attention.
  * top_k:       at least 1; sink_blocks + recent_blocks may not exceed it.
  * block_list:  [rows][top_k] int32: logical page indexes, ascending, then -1.
  * block_count: [rows] int32: min(top_k, the row's visible pages).  A row whose length is out of range is
@@ -459,7 +461,8 @@ size_t kvc_block_attention_workspace_bytes(int32_t rows, int32_t group, int32_t 
  * Attention of one new token over the listed pages of each row, or over the whole row: out and lse as for
  * kvc_decode_attention (same q, q_pos and masking by slot_pos), over the slots below row_len of the pages
  * block_list[row][0 .. block_count[row] - 1].  No scores are kept, so rows may have any length, and the work is split evenly
- * over the GPU whatever the number of rows and their lengths.
+ * over the GPU whatever the number of rows and their lengths: the call for attention alone (kvc_decode_attention also
+ * gives each entry's score).  The sums that are divided at the end are fp32: values' magnitudes, summed over a row, below 2^119.
  * block_list:  [rows][list_stride] int32 logical pages, strictly ascending (kvc_select_blocks' list with list_stride =
  *              top_k), or NULL for all pages (list_stride and block_count are then not used).
  * block_count: [rows] int32 in [0, list_stride].
