@@ -10,13 +10,15 @@ matter for it.
 with torch and marshals arguments.  After a compaction, which frees pages and moves entries between the others, call ``reclaim``
 with its freed list: the pages go back on the stack, so that they go round between eviction and new tokens, and the bounds are
 taken anew.  The freed list of an ``EvictionRound`` (its ``freed`` and ``num_freed``) can be the stack itself only until
-that round runs again: a compaction begins its list anew, and what is left on it would be lost.  The tokens of a call bring the queries, keys and values of all layers of the cache at once, so a model whose
-layers depend on one another keeps a cache and a ServingStep for each layer; and decode brings a token for every sequence (a
-batch with finished requests makes the calls itself, with counts of 0).
+that round runs again: a compaction begins its list anew, and what is left on it would be lost.
 
-The constructor works on the current stream of the cache's device.  All calls take device tensors and do not synchronise, so a step can be captured into a
-CUDA graph; two graphs of one ServingStep share its buffers and must not overlap.  A call whose arguments are refused
-(kvc.KvcError) is refused before anything is enqueued: the cache and the stack are as they were.
+The tokens of a call bring the queries, keys and values of all layers of the cache at once, so a model whose layers depend on one
+another keeps a cache and a ServingStep for each layer; and decode brings a token for every sequence (a batch with finished
+requests makes the calls itself, with counts of 0).
+
+The constructor works on the current stream of the cache's device.  All calls take device tensors and do not synchronise, so a
+step can be captured into a CUDA graph; two graphs of one ServingStep share its buffers and must not overlap.  A call whose
+arguments are refused (kvc.KvcError) is refused before anything is enqueued: the cache and the stack are as they were.
 """
 from __future__ import annotations
 
@@ -113,6 +115,8 @@ class ServingStep:
         """The stream of a call as torch has it, and a handle's for a number (None: the current one of the cache's device)."""
         if stream is None or hasattr(stream, "cuda_stream"):
             return stream
+        if not 0 <= int(stream) < 1 << 64:
+            raise kvc.KvcError(f"stream: {stream} is no stream")
         return torch.cuda.ExternalStream(int(stream), device=self.cache.k_pool.device)
 
     def refresh(self, stream=None):

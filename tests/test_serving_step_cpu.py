@@ -65,3 +65,10 @@ def test_calls_are_refused_before_anything_is_enqueued(monkeypatch):
     with pytest.raises(kvc.KvcError, match="together"):
         late.decode(x(), pos)
     assert called == []
+
+
+def test_a_number_that_is_no_stream():
+    for bad in (-1, 1 << 64, 1 << 70):
+        with pytest.raises(kvc.KvcError, match="no stream"):
+            make()._stream(bad)
+    assert make()._stream(None) is None
